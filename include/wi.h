@@ -86,6 +86,8 @@ typedef enum wi_dtype { WI_F32 = 0, WI_BF16 = 1 } wi_dtype;
                                     precision: the index's centroids are not the
                                     means of their members (every index the
                                     build calls write is); results not valid    */
+#define WI_DEV_NO_PAGES 0x40u    /* wi_plan_pages: too few free pages, a table row
+                                    or the slot map too short; nothing was planned */
 
 /*
  * Paged KV cache in original token order (the build input).
@@ -383,6 +385,116 @@ wi_status wi_decode_noalloc(const void *q, const wi_index *idx, const wi_decode_
 /* Number of kernels one wi_decode call launches, and its stage names. */
 int32_t wi_decode_stage_count(void);
 const char *wi_decode_stage_name(int32_t i);
+
+/* ---------------------------------------------------------------- serving */
+
+/*
+ * The step in front of the build and decode calls: which pages a batch's new
+ * tokens go to, their key and value rows written there, and their attention
+ * over the cache (a prompt, a chunk of one, or single tokens that no index
+ * covers yet).  Page-centred tensors with index pointers are the layout of
+ * Vortex 2.B (vTensor); the calls are this library's own.
+ */
+
+/*
+ * Block tables and slot maps of one step, from the requests' lengths on the
+ * GPU.  Request b has seq_lens[b] tokens in the cache and gets new_lens[b]
+ * more (either may be 0).  Its page count grows from ceil(have/P) to
+ * ceil((have+new)/P); the pages come off the end of the stack free_pages
+ * (request 0 first, each request's pages in order: the first page taken is
+ * free_pages[*n_free - 1]) and are written to its row of block_table behind
+ * those in use.  Other entries of the table stay as they are.
+ *   starts[b]     first new token of request b in the packed step (starts[batch]
+ *                 is their count)
+ *   slot_map[i]   page * P + row of packed token i; -1 behind the last token
+ *   positions[i]  its position in its sequence; -1 behind the last token
+ *   seq_lens_out, n_free_out   the lengths and the stack's size after the step;
+ *                 they may be seq_lens and n_free themselves (a captured step
+ *                 then advances each time it is replayed)
+ * All or nothing: with too few free pages, a table row shorter than a request
+ * needs, more tokens than `capacity` (WI_DEV_NO_PAGES), a negative or
+ * overflowing length (WI_DEV_BAD_SLOT) or *n_free outside [0, max_free]
+ * (WI_DEV_BAD_PAGE), the table keeps its entries, slot_map and positions are
+ * all -1, starts all 0, and the lengths and stack size stay.  A free page id
+ * outside [0, n_pages) sets WI_DEV_BAD_PAGE; its entry and slots become -1.
+ * Freed pages are pushed by the caller: written behind the stack's end.
+ * No two buffers may overlap, but for the two in-place pairs.
+ */
+typedef struct wi_page_plan {
+  int32_t batch;               /* 1..WI_MAX_BATCH                               */
+  int32_t page_size;           /* power of two, 1..1024                         */
+  int64_t n_pages;             /* pages of the pools; n_pages * P <= INT32_MAX  */
+  const int32_t *seq_lens;     /* device [batch]                                */
+  const int32_t *new_lens;     /* device [batch]                                */
+  int32_t *block_table;        /* device [batch][max_pages]                     */
+  int32_t max_pages;
+  const int32_t *free_pages;   /* device [max_free]                             */
+  int32_t max_free;            /* >= 0; free_pages may be null when it is 0     */
+  const int32_t *n_free;       /* device [1]                                    */
+  int32_t *seq_lens_out;       /* device [batch]                                */
+  int32_t *n_free_out;         /* device [1]                                    */
+  int32_t *starts;             /* device [batch + 1]                            */
+  int32_t capacity;            /* entries of slot_map and positions, >= 0       */
+  int32_t *slot_map;           /* device [capacity]                             */
+  int32_t *positions;          /* device [capacity], or null                    */
+} wi_page_plan;
+
+/* Workspace of wi_plan_pages and wi_append_kv: its first 256 bytes. */
+#define WI_SERVE_WORKSPACE 256
+
+wi_status wi_plan_pages(const wi_page_plan *p, void *ws, size_t ws_bytes, wi_stream_t stream);
+
+/*
+ * Write a step's key and value rows into the paged pools: row (i, h) of k and
+ * v goes to pool[slot_map[i] / P][h][slot_map[i] % P].  A negative slot skips
+ * its token; one outside the pool is skipped and sets WI_DEV_BAD_SLOT.  Two
+ * tokens of a call must not have the same slot.  Rows not named stay as they
+ * are.  Head h of token i is at k + i * k_stride + h * head_dim.
+ */
+typedef struct wi_kv_append {
+  wi_dtype dtype;              /* of rows and pools                             */
+  int32_t n_tokens;            /* >= 0                                          */
+  int32_t n_kv_heads;          /* >= 1                                          */
+  int32_t head_dim;            /* 64 or 128                                     */
+  int32_t page_size;           /* power of two, 1..1024                         */
+  int64_t n_pages;
+  const void *k, *v;           /* device rows                                   */
+  int64_t k_stride, v_stride;  /* elements between tokens: a multiple of 16 bytes,
+                                  >= Hkv * d; 0 = Hkv * d                       */
+  const int32_t *slot_map;     /* device [n_tokens]                             */
+  void *k_pool, *v_pool;       /* device [n_pages][Hkv][P][d]                   */
+} wi_kv_append;
+
+wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stream_t stream);
+
+/*
+ * Causal attention of packed queries over the paged cache in original order.
+ * The queries of sequence b are those of its last q_lens[b] tokens: query i
+ * sits at position T_b - q_lens[b] + i and attends every position up to its
+ * own.  q_lens[b] = T_b is a whole prompt, 1 a decode step, 0 leaves the
+ * sequence out.  For query head g, KV head g / G:
+ *   out = sum_p softmax_p(q . k_p / sqrt(d)) v_p,  lse = ln sum_p e^(q . k_p / sqrt(d))
+ * q:   device [sum q_lens][Hq][d] in the KV dtype, sequences in order, token
+ *      rows q_stride elements apart.
+ * out: device, like q with out_stride (KV dtype: the next product's input).
+ *      Not q itself.  Rows behind the last sequence are not written.
+ * lse: device float [sum q_lens][Hq], or NULL.
+ * Keys behind a query's position have no effect on it, whatever they hold
+ * (NaN and infinities too), nor have pool rows behind T_b.  bf16 rounds the
+ * softmax weights to bf16 for the product with the values; their sum and the
+ * accumulators are fp32.
+ */
+typedef struct wi_attend_params {
+  int32_t n_q_heads;           /* Hq, a multiple of Hkv with G in {1,2,4,8}     */
+  const int32_t *q_lens;       /* host [batch], 0 <= q_lens[b] <= T_b; NULL = T_b */
+  int64_t q_stride;            /* elements: a multiple of 16 bytes, >= Hq * d;
+                                  0 = Hq * d                                    */
+  int64_t out_stride;          /* likewise                                      */
+} wi_attend_params;
+
+wi_status wi_attend_workspace_size(const wi_kv_cache *kv, const wi_attend_params *p, size_t *bytes);
+wi_status wi_attend(const void *q, const wi_kv_cache *kv, const wi_attend_params *p, void *out,
+                    float *lse, void *ws, size_t ws_bytes, wi_stream_t stream);
 
 /* --------------------------------------------------------------- status */
 

@@ -40,7 +40,8 @@ WI_MAX_BATCH = 256
 WI_MAX_SEG_LEN = 16384
 WI_MAX_STEADY = 8192
 WI_DEV_BAD_PAGE, WI_DEV_BAD_SLOT, WI_DEV_BAD_CLUSTER, WI_DEV_BAD_HIST = 0x1, 0x2, 0x4, 0x8
-WI_DEV_TIMEOUT, WI_DEV_CANCELLATION = 0x10, 0x20
+WI_DEV_TIMEOUT, WI_DEV_CANCELLATION, WI_DEV_NO_PAGES = 0x10, 0x20, 0x40
+WI_SERVE_WORKSPACE = 256
 WI_TOPK_EXACT, WI_TOPK_SAMPLED = 0, 1
 
 EXPORTED = [
@@ -51,6 +52,7 @@ EXPORTED = [
     "wi_decode_workspace_size", "wi_decode_workspace_layout", "wi_decode", "wi_decode_host",
     "wi_decode_stage_count", "wi_decode_stage_name", "wi_read_device_status",
     "wi_status_string", "wi_last_error_string", "wi_decode_noalloc",
+    "wi_plan_pages", "wi_append_kv", "wi_attend_workspace_size", "wi_attend",
 ]
 
 
@@ -91,6 +93,28 @@ class WiDecodeLayout(C.Structure):
                 ("info_ints", C.c_int32)]
 
 
+class WiPagePlan(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int64),
+                ("seq_lens", C.c_void_p), ("new_lens", C.c_void_p), ("block_table", C.c_void_p),
+                ("max_pages", C.c_int32), ("free_pages", C.c_void_p), ("max_free", C.c_int32),
+                ("n_free", C.c_void_p), ("seq_lens_out", C.c_void_p), ("n_free_out", C.c_void_p),
+                ("starts", C.c_void_p), ("capacity", C.c_int32), ("slot_map", C.c_void_p),
+                ("positions", C.c_void_p)]
+
+
+class WiKVAppend(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("n_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int64),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("slot_map", C.c_void_p), ("k_pool", C.c_void_p),
+                ("v_pool", C.c_void_p)]
+
+
+class WiAttendParams(C.Structure):
+    _fields_ = [("n_q_heads", C.c_int32), ("q_lens", C.POINTER(C.c_int32)),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64)]
+
+
 _P = C.c_void_p
 _sig = {
     "wi_index_clusters": (C.c_int, [C.c_int32, C.POINTER(C.c_int32), C.c_int32, C.c_int32,
@@ -117,6 +141,12 @@ _sig = {
                                  C.c_size_t, _P]),
     "wi_decode_noalloc": (C.c_int, [_P, C.POINTER(WiIndex), C.POINTER(WiDecodeParams), _P, _P,
                                     _P]),
+    "wi_plan_pages": (C.c_int, [C.POINTER(WiPagePlan), _P, C.c_size_t, _P]),
+    "wi_append_kv": (C.c_int, [C.POINTER(WiKVAppend), _P, C.c_size_t, _P]),
+    "wi_attend_workspace_size": (C.c_int, [C.POINTER(WiKVCache), C.POINTER(WiAttendParams),
+                                           C.POINTER(C.c_size_t)]),
+    "wi_attend": (C.c_int, [_P, C.POINTER(WiKVCache), C.POINTER(WiAttendParams), _P, _P, _P,
+                            C.c_size_t, _P]),
     "wi_decode_stage_count": (C.c_int32, []),
     "wi_decode_stage_name": (C.c_char_p, [C.c_int32]),
     "wi_read_device_status": (C.c_int, [_P, _P, C.POINTER(C.c_uint32), C.c_int]),
@@ -533,6 +563,234 @@ def decode_noalloc(q: torch.Tensor, index: WaveIndex, params: DecodeParams,
     ix, p = index.c_struct(), params.c_struct()
     _check(_lib.wi_decode_noalloc(_ptr(q), C.byref(ix), C.byref(p), _ptr(out), _ptr(lse),
                                   _stream_ptr(stream)), "wi_decode_noalloc")
+    return out, lse
+
+
+# ---------------------------------------------------------------- serving
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_gpu(name: str, t: torch.Tensor, dtype, like: Optional[torch.Tensor] = None, shape=None):
+    """Argument checks of the serving calls (the library sees only pointers)."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor is expected, got "
+                         f"{t.dtype} on {t.device}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors on {like.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _token_rows(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
+    """Checks [tokens][heads][d] rows (a view of wider rows is fine: only the
+    token stride may differ from contiguous); returns the token stride."""
+    _need(t.dim() == 3 and t.dtype == like.dtype and t.device == like.device,
+          f"{name}: a [tokens][heads][head_dim] {like.dtype} tensor on {like.device} is expected")
+    n, heads, d = t.shape
+    _need((d == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d),
+          f"{name}: the heads of a token must be contiguous")
+    _need(n <= 1 or t.stride(0) >= heads * d, f"{name}: token rows must not overlap")
+    return t.stride(0) if n > 1 else heads * d
+
+
+class _Here:
+    """The call's stream on the tensors' device, and that device current for
+    the launch.  Tensors the call allocates are allocated on that stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        _need(self.stream.device == t.device,
+              f"the stream is on {self.stream.device}, the tensors on {t.device}")
+        self.guard = None
+        if stream is not None or t.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return C.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+@dataclass
+class PageTable:
+    """A batch's pages, on the GPU: block_table [batch][max_pages], seq_lens
+    [batch] and the stack of free pages, free_pages [<= n_pages] of which the
+    first n_free[0] entries are free (all int32)."""
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+    free_pages: torch.Tensor
+    n_free: torch.Tensor
+    page_size: int
+    n_pages: int
+
+    @classmethod
+    def empty(cls, batch: int, max_pages: int, page_size: int, n_pages: int, device) -> "PageTable":
+        """No tokens yet, every page free (page 0 is handed out first)."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((batch, max_pages), -1, **i32), torch.zeros(batch, **i32),
+                   torch.arange(n_pages - 1, -1, -1, **i32), torch.full((1,), n_pages, **i32),
+                   page_size, n_pages)
+
+
+@dataclass
+class PagePlan:
+    """What plan_pages writes (all int32; see wi_page_plan in include/wi.h)."""
+    slot_map: torch.Tensor       # [capacity]
+    positions: torch.Tensor      # [capacity]
+    starts: torch.Tensor         # [batch + 1]
+    seq_lens: torch.Tensor       # [batch]
+    n_free: torch.Tensor         # [1]
+
+    @classmethod
+    def empty(cls, table: PageTable, capacity: int, update: bool = False) -> "PagePlan":
+        """Buffers for plans of up to `capacity` tokens.  With update, the
+        lengths and the stack's size are the table's own: the plan advances it."""
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=table.block_table.device)
+        B = table.block_table.shape[0]
+        return cls(new(capacity), new(capacity), new(B + 1), table.seq_lens if update else new(B),
+                   table.n_free if update else new(1))
+
+
+def serve_workspace(device) -> torch.Tensor:
+    """Workspace of plan_pages and append_kv."""
+    return workspace(WI_SERVE_WORKSPACE, device)
+
+
+def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
+               out: Optional[PagePlan] = None, update: bool = False,
+               ws: Optional[torch.Tensor] = None, stream=None) -> PagePlan:
+    """Pages and slots for new_lens [batch] more tokens of each request
+    (wi_plan_pages).  Writes the new pages to table.block_table; table.seq_lens
+    and table.n_free advance too with update (or with an `out` that holds them),
+    else the plan returns the new ones.  `capacity` bounds the step's tokens;
+    slots and positions behind the last one are -1.  A step that does not fit
+    plans nothing and sets WI_DEV_NO_PAGES in the workspace's status."""
+    bt = table.block_table
+    _need(bt.dim() == 2, "block_table: [batch][max_pages] is expected")
+    B = bt.shape[0]
+    _on_gpu("block_table", bt, torch.int32)
+    _on_gpu("seq_lens", table.seq_lens, torch.int32, bt, (B,))
+    _on_gpu("new_lens", new_lens, torch.int32, bt, (B,))
+    _on_gpu("free_pages", table.free_pages, torch.int32, bt, (table.free_pages.numel(),))
+    _on_gpu("n_free", table.n_free, torch.int32, bt, (1,))
+    with _Here(bt, stream) as s:
+        if out is None:
+            out = PagePlan.empty(table, capacity, update)
+        else:
+            _need(not update or (out.seq_lens is table.seq_lens and out.n_free is table.n_free),
+                  "update: `out` must hold the table's own seq_lens and n_free")
+            _on_gpu("out.slot_map", out.slot_map, torch.int32, bt, (capacity,))
+            _on_gpu("out.positions", out.positions, torch.int32, bt, (capacity,))
+            _on_gpu("out.starts", out.starts, torch.int32, bt, (B + 1,))
+            _on_gpu("out.seq_lens", out.seq_lens, torch.int32, bt, (B,))
+            _on_gpu("out.n_free", out.n_free, torch.int32, bt, (1,))
+        if ws is None:
+            ws = serve_workspace(bt.device)
+        _on_gpu("ws", ws, torch.uint8, bt)
+        p = WiPagePlan(B, table.page_size, table.n_pages, table.seq_lens.data_ptr(),
+                       new_lens.data_ptr(), bt.data_ptr(), bt.shape[1],
+                       table.free_pages.data_ptr(), table.free_pages.numel(),
+                       table.n_free.data_ptr(), out.seq_lens.data_ptr(), out.n_free.data_ptr(),
+                       out.starts.data_ptr(), capacity, out.slot_map.data_ptr(),
+                       out.positions.data_ptr())
+        _check(_lib.wi_plan_pages(C.byref(p), _ptr(ws), ws.numel(), s), "wi_plan_pages")
+    return out
+
+
+def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: torch.Tensor,
+              v_pool: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write k, v [tokens][n_kv_heads][head_dim] into the pools' rows at
+    slot_map [tokens] (wi_append_kv).  Negative slots are skipped; k and v may
+    be views of a fused projection's rows."""
+    _need(k_pool.dim() == 4 and k_pool.shape == v_pool.shape,
+          "k_pool, v_pool: equal [n_pages][n_kv_heads][page_size][head_dim] shapes are expected")
+    _on_gpu("k_pool", k_pool, k_pool.dtype)
+    _on_gpu("v_pool", v_pool, k_pool.dtype, k_pool)
+    n_pages, H, P, d = k_pool.shape
+    ks, vs = _token_rows("k", k, k_pool), _token_rows("v", v, k_pool)
+    n = k.shape[0]
+    _need(tuple(k.shape) == tuple(v.shape) == (n, H, d), f"k, v: [tokens][{H}][{d}] is expected")
+    _on_gpu("slot_map", slot_map, torch.int32, k_pool, (n,))
+    with _Here(k_pool, stream) as s:
+        if ws is None:
+            ws = serve_workspace(k_pool.device)
+        _on_gpu("ws", ws, torch.uint8, k_pool)
+        a = WiKVAppend(_dtype_code(k_pool.dtype), n, H, d, P, n_pages, k.data_ptr(), v.data_ptr(),
+                       ks, vs, slot_map.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
+        _check(_lib.wi_append_kv(C.byref(a), _ptr(ws), ws.numel(), s), "wi_append_kv")
+
+
+@dataclass
+class AttendParams:
+    """q_lens[b]: query tokens of sequence b, its last ones (None: all of them)."""
+    n_q_heads: int
+    q_lens: Optional[List[int]] = None
+
+    def __post_init__(self):
+        self._q_lens = None if self.q_lens is None else _i32_array(self.q_lens)
+
+    def n_queries(self, kv: KVCache) -> int:
+        _need(self._q_lens is None or len(self._q_lens) == len(kv.seq_lens),
+              "q_lens: one entry per sequence is expected")
+        return sum(kv.seq_lens if self._q_lens is None else self._q_lens)
+
+    def c_struct(self, q_stride: int = 0, out_stride: int = 0) -> WiAttendParams:
+        q_lens = None if self._q_lens is None else C.cast(self._q_lens, C.POINTER(C.c_int32))
+        return WiAttendParams(self.n_q_heads, q_lens, q_stride, out_stride)
+
+
+def attend_workspace_bytes(kv: KVCache, params: AttendParams) -> int:
+    params.n_queries(kv)
+    n = C.c_size_t()
+    s, p = kv.c_struct(), params.c_struct()
+    _check(_lib.wi_attend_workspace_size(C.byref(s), C.byref(p), C.byref(n)),
+           "wi_attend_workspace_size")
+    return n.value
+
+
+def attend_workspace(kv: KVCache, params: AttendParams) -> torch.Tensor:
+    return workspace(attend_workspace_bytes(kv, params), kv.k_pool.device)
+
+
+def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[torch.Tensor] = None,
+           lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of the sequences' last q_lens tokens over the paged
+    cache (wi_attend): q [sum q_lens][n_q_heads][head_dim] in the KV dtype,
+    sequences in order (rows may be views of wider ones) -> out like q, lse
+    fp32 [sum q_lens][n_q_heads].  q may have rows behind the last sequence
+    (a padded batch): out and lse keep theirs."""
+    kp = kv.k_pool
+    qs = _token_rows("q", q, kp)
+    n, Hq, d = q.shape
+    _need(Hq == params.n_q_heads and d == kv.head_dim,
+          f"q: [tokens][{params.n_q_heads}][{kv.head_dim}] is expected")
+    _need(n >= params.n_queries(kv), "q: fewer rows than sum(q_lens)")
+    _need(kv.v_pool.shape == kp.shape and kv.block_table.dim() == 2
+          and kv.block_table.shape[0] == len(kv.seq_lens), "kv: pools and table do not match")
+    _on_gpu("k_pool", kp, kp.dtype)
+    _on_gpu("v_pool", kv.v_pool, kp.dtype, kp)
+    _on_gpu("block_table", kv.block_table, torch.int32, kp)
+    with _Here(kp, stream) as s:
+        if out is None:
+            out = torch.empty(n, Hq, d, dtype=q.dtype, device=q.device)
+        os_ = _token_rows("out", out, kp)
+        _need(out.shape == q.shape, "out: the shape of q is expected")
+        if lse is None:
+            lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
+        _on_gpu("lse", lse, torch.float32, kp, (n, Hq))
+        if ws is None:
+            ws = attend_workspace(kv, params)
+        _on_gpu("ws", ws, torch.uint8, kp)
+        c, p = kv.c_struct(), params.c_struct(qs, os_)
+        _check(_lib.wi_attend(_ptr(q), C.byref(c), C.byref(p), _ptr(out), _ptr(lse), _ptr(ws),
+                              ws.numel(), s), "wi_attend")
     return out, lse
 
 

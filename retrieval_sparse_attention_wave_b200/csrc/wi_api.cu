@@ -16,17 +16,23 @@
 #include "wi.h"
 #include "wi_common.cuh"
 #include "wi_plan.h"
+#include "wi_serve.h"
 
 namespace wi {
 namespace {
 
 thread_local char g_last_error[256] = "";
 
+}  // namespace
+
+// WI_ERR_CUDA, with the error kept for wi_last_error_string (every entry point's)
 wi_status cuda_fail(cudaError_t e) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", cudaGetErrorName(e),
                 cudaGetErrorString(e));
   return WI_ERR_CUDA;
 }
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -40,6 +46,8 @@ int64_t clusters_of(int64_t T, int S, int cs) {
 }
 
 int esize(wi_dtype d) { return d == WI_BF16 ? 2 : 4; }
+
+}  // namespace
 
 // Common geometry checks for a paged pool description.
 wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int64_t n_pages,
@@ -63,6 +71,8 @@ wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int6
   if (tot * hkv > INT32_MAX) return WI_ERR_UNSUPPORTED;
   return WI_OK;
 }
+
+namespace {
 
 wi_status check_seg(int S, int cs) {
   if (S < 1 || cs < 1 || S % cs != 0) return WI_ERR_INVALID_ARG;

@@ -1,0 +1,411 @@
+// Causal attention of packed queries over the paged cache (wi_attend).
+//
+// Row r of a block holds a query q_r at position pos_r; over the key tiles
+// t = 0, 1, ... its running maximum, mass and output
+//   m' = max(m, max_k s_rk),  c = 2^(m - m'),
+//   l' = c l + sum_k 2^(s_rk - m'),  o' = c o + sum_k 2^(s_rk - m') v_k
+// (s in units of log2 e / sqrt(d); s_rk = -inf for k > pos_r) end as
+// out = o / l and lse = ln2 (m + log2 l): one pass over the keys, nothing of
+// size queries x keys in memory.  Key runs of a split block end as parts
+// (m, l, o), which attend_merge_kernel joins by the same rule.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "wi_serve.h"
+
+namespace wi {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttendTable {
+  int32_t n_seq, n_items, hkv, g_shift, rows;
+  AttendSeq seq[kMaxBatch];
+};
+
+// One item of the plan, as its CTA needs it.
+struct Item {
+  int b, h, T, n, q0;
+  int row0, rows;       // its rows of the unit
+  int pos0;             // position of query token 0 of the sequence
+  int key_end;          // keys its last row sees
+  int t0, t1;           // key tiles
+  int64_t part;         // first part row, -1: the whole key range
+};
+
+__device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT) {
+  int lo = 0, hi = tb.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.seq[mid].item0 <= item) lo = mid; else hi = mid - 1;
+  }
+  const AttendSeq& s = tb.seq[lo];
+  Item it;
+  const int x = item - s.item0, split = x % s.ns, y = x / s.ns;
+  const int blk = s.nblk - 1 - y / tb.hkv, all = s.n << tb.g_shift;
+  it.h = y % tb.hkv;
+  it.b = s.b; it.T = s.T; it.n = s.n; it.q0 = s.q0;
+  it.row0 = blk * tb.rows;
+  it.rows = min(tb.rows, all - it.row0);
+  it.pos0 = s.T - s.n;
+  it.key_end = it.pos0 + ((it.row0 + it.rows - 1) >> tb.g_shift) + 1;
+  const int64_t nt = (it.key_end + KT - 1) / KT;
+  it.t0 = (int)(nt * split / s.ns);
+  it.t1 = (int)(nt * (split + 1) / s.ns);
+  it.part = -1;
+  if (s.ns > 1)
+    it.part = s.part0 + (((int64_t)blk * tb.hkv + it.h) * s.ns + split) * min(tb.rows, all);
+  return it;
+}
+
+struct AttendOut {
+  void* out;
+  float* lse;
+  float2* ml;
+  float* o;
+  int64_t stride;
+  int Hq;
+};
+
+// ------------------------------------------------------------ FMA kernel
+// 128 threads, 16 of them (half a warp) share a row group of RT rows: each
+// takes every 16th key of a tile and every 16th 16-byte chunk of the output
+// columns, so a row's statistics and weights stay inside its half warp.
+// Products run on packed fp32 FMAs (two head channels at a time).
+template <typename T, int D, int RT>
+struct FmaShape {
+  static constexpr int kThreads = 128;
+  static constexpr int R = 8 * RT;
+  static constexpr int KT = D == 128 ? 32 : 64;
+  static constexpr int KPT = KT / 16;      // keys per thread
+  static constexpr int CPT = D / 64;       // 16-byte output chunks per thread
+  static constexpr int LD = D + 4;         // padded row: 8 rows on 8 different bank groups
+  static constexpr int PLD = KT + 4;
+  static constexpr size_t kSmem = (size_t)(R * LD + 2 * KT * LD + R * PLD) * 4;
+};
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(128)
+attend_fma_kernel(const __grid_constant__ AttendTable tb, const void* __restrict__ q_, int64_t q_stride,
+                  const Pool kp, const Pool vp, const AttendOut ao, float scale, uint32_t* status) {
+  using S = FmaShape<T, D, RT>;
+  extern __shared__ __align__(16) float sh_fma[];
+  float* sq = sh_fma;
+  float* sk = sq + S::R * S::LD;
+  float* sv = sk + S::KT * S::LD;
+  float* sp = sv + S::KT * S::LD;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_launch_dependents();
+  const Item it = item_of(tb, blockIdx.x, S::KT);
+  const int G = 1 << tb.g_shift;
+  constexpr int VE = Elem<T>::kPerVec, CH = D / VE;
+
+  // rows [base, base + KT) of a pool into a tile; rows behind key_end are zero
+  auto load_tile = [&](const Pool& p, float* dst, int base) {
+    for (int c = tid; c < S::KT * CH; c += 128) {
+      const int r = c / CH, ch = c % CH;
+      const int64_t row = base + r < it.key_end ? pool_row(p, tb.hkv, D, it.b, it.h, base + r, status) : -1;
+      float* to = dst + r * S::LD + ch * VE;
+      const T* from = reinterpret_cast<const T*>(p.base) + row + ch * VE;
+      if (row < 0) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) to[e] = 0.f;
+      } else if constexpr (sizeof(T) == 4) {
+        cp_async16(to, from);
+      } else {
+        float x[VE];
+        Elem<T>::unpack(ld_stream(from), x);
+#pragma unroll
+        for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      }
+    }
+    cp_async_commit();
+  };
+
+  if (it.t0 < it.t1) load_tile(kp, sk, it.t0 * S::KT);
+  for (int c = tid; c < S::R * CH; c += 128) {
+    const int r = c / CH, ch = c % CH;
+    float x[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) x[e] = 0.f;
+    if (r < it.rows) {
+      const int row = it.row0 + r;
+      const T* from = reinterpret_cast<const T*>(q_) + (int64_t)(it.q0 + (row >> tb.g_shift)) * q_stride +
+                      (int64_t)(it.h * G + (row & (G - 1))) * D + ch * VE;
+      Elem<T>::unpack(ld_stream(from), x);
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sq[r * S::LD + ch * VE + e] = x[e] * scale;
+  }
+  float m[RT], l[RT];
+  float4 o[RT][S::CPT];
+  int pos[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    pos[i] = it.pos0 + ((it.row0 + ty * RT + i) >> tb.g_shift);
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
+
+  for (int t = it.t0; t < it.t1; ++t) {
+    const int base = t * S::KT;
+    load_tile(vp, sv, base);
+    cp_async_wait<1>();
+    __syncthreads();
+    float s[RT][S::KPT];
+    {
+      float2 a[RT][S::KPT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::KPT; ++j) a[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int c = 0; c < D / 4; ++c) {
+        float4 kk[S::KPT];
+#pragma unroll
+        for (int j = 0; j < S::KPT; ++j) kk[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * S::LD + 4 * c);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float4 qq = *reinterpret_cast<const float4*>(sq + (ty * RT + i) * S::LD + 4 * c);
+#pragma unroll
+          for (int j = 0; j < S::KPT; ++j) {
+            a[i][j] = __ffma2_rn(make_float2(qq.x, qq.y), make_float2(kk[j].x, kk[j].y), a[i][j]);
+            a[i][j] = __ffma2_rn(make_float2(qq.z, qq.w), make_float2(kk[j].z, kk[j].w), a[i][j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::KPT; ++j) s[i][j] = a[i][j].x + a[i][j].y;
+    }
+    __syncthreads();   // the key tile is free
+    if (t + 1 < it.t1) load_tile(kp, sk, base + S::KT);
+    else cp_async_commit();
+    const bool diag = base + S::KT - 1 > first_pos;   // some row does not see all of the tile
+    if (diag) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::KPT; ++j)
+          if (base + tx + 16 * j > pos[i]) s[i][j] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      float mx = s[i][0];
+#pragma unroll
+      for (int j = 1; j < S::KPT; ++j) mx = fmaxf(mx, s[i][j]);
+#pragma unroll
+      for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(m[i], mx);
+      const float mu = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: weights 0, not NaN
+      const float c = exp2f(m[i] - mu);
+      m[i] = mn;
+      l[i] *= c;
+#pragma unroll
+      for (int j = 0; j < S::KPT; ++j) {
+        const float p = exp2f(s[i][j] - mu);
+        l[i] += p;
+        sp[(ty * RT + i) * S::PLD + tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int cc = 0; cc < S::CPT; ++cc) {
+        o[i][cc].x *= c; o[i][cc].y *= c; o[i][cc].z *= c; o[i][cc].w *= c;
+      }
+    }
+    cp_async_wait<1>();
+    __syncthreads();   // the value tile and the weights are there
+    // a masked weight is 0, but 0 * NaN is not: on the diagonal the masked
+    // keys are left out of the sum instead of added with weight 0
+    auto accumulate = [&](auto masked) {
+#pragma unroll 2
+      for (int k = 0; k < S::KT; k += 4) {
+        float4 p[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * RT + i) * S::PLD + k);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+          for (int cc = 0; cc < S::CPT; ++cc) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + (k + u) * S::LD + 4 * (tx + 16 * cc));
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+              if (masked && base + k + u > pos[i]) continue;
+              float2 lo = make_float2(o[i][cc].x, o[i][cc].y), hi = make_float2(o[i][cc].z, o[i][cc].w);
+              lo = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), lo);
+              hi = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), hi);
+              o[i][cc] = make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+          }
+        }
+      }
+    };
+    if (diag) accumulate(std::true_type{});
+    else accumulate(std::false_type{});
+    __syncthreads();   // the value tile and the weights are free
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+#pragma unroll
+    for (int x = 8; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+    const int r = ty * RT + i;
+    if (r >= it.rows) continue;
+    if (it.part >= 0) {
+      if (tx == 0) ao.ml[it.part + r] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int cc = 0; cc < S::CPT; ++cc)
+        *reinterpret_cast<float4*>(ao.o + (it.part + r) * D + 4 * (tx + 16 * cc)) = o[i][cc];
+    } else {
+      const int row = it.row0 + r;
+      const int64_t tok = it.q0 + (row >> tb.g_shift);
+      const int head = it.h * G + (row & (G - 1));
+      if (tx == 0 && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m[i] + log2f(l[i]));
+      T* to = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D;
+      const float inv = 1.f / l[i];
+#pragma unroll
+      for (int cc = 0; cc < S::CPT; ++cc) {
+        const float4 x = make_float4(o[i][cc].x * inv, o[i][cc].y * inv, o[i][cc].z * inv, o[i][cc].w * inv);
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to + 4 * (tx + 16 * cc)) = x;
+        else *reinterpret_cast<uint2*>(to + 4 * (tx + 16 * cc)) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// One warp per query row of the split sequences: the parts' (m, l) give the
+// weights 2^(m_s - m), then the parts' outputs are added in order.
+constexpr int kMergeThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads)
+attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const AttendOut ao) {
+  constexpr int E = D / 32;   // columns per lane
+  const int lane = threadIdx.x & 31;
+  const int x = blockIdx.x * (kMergeThreads / 32) + ((int)threadIdx.x >> 5);
+  int lo = 0, hi = tb.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.seq[mid].mrow0 <= x) lo = mid; else hi = mid - 1;
+  }
+  const AttendSeq& s = tb.seq[lo];
+  const int all = s.n << tb.g_shift, Rb = min(tb.rows, all);
+  const int h = (x - s.mrow0) / all, row = (x - s.mrow0) % all;
+  const int blk = row / tb.rows, rr = row % tb.rows;
+  const int64_t part = s.part0 + ((int64_t)blk * tb.hkv + h) * s.ns * Rb + rr;
+  pdl_wait();   // the parts are there
+  if (x >= n_rows) return;
+  float m = -INFINITY;
+  for (int i = lane; i < s.ns; i += 32) m = fmaxf(m, __ldcg(&ao.ml[part + (int64_t)i * Rb]).x);
+  m = warp_max(m);
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int i0 = 0; i0 < s.ns; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < s.ns) {
+      const float2 ml = __ldcg(&ao.ml[part + (int64_t)(i0 + lane) * Rb]);
+      w = exp2f(ml.x - mu);
+      l = fmaf(w, ml.y, l);
+    }
+    const int n = min(32, s.ns - i0);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* from = ao.o + (part + (int64_t)(i0 + i) * Rb) * D + lane * E;
+      float v[E];
+      if constexpr (E == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(from));
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(from));
+        v[0] = f.x; v[1] = f.y;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(wi, v[e], o[e]);
+    }
+  }
+  l = warp_sum(l);
+  const int64_t tok = s.q0 + (row >> tb.g_shift);
+  const int head = (h << tb.g_shift) + (row & ((1 << tb.g_shift) - 1));
+  if (lane == 0 && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m + log2f(l));
+  const float inv = 1.f / l;
+  T* to = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) store_elem(to + e, o[e] * inv);
+}
+
+int log2_of(int x) { int r = 0; while ((1 << r) < x) ++r; return r; }
+
+// Dynamic shared memory limit of a kernel, raised once per device.
+template <auto kern>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};   // one bit per device (the first 64)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendOut& ao, float scale,
+                       uint32_t* status, cudaStream_t s) {
+  using S = FmaShape<T, D, RT>;
+  const cudaError_t e = allow_smem<attend_fma_kernel<T, D, RT>>(S::kSmem);
+  if (e != cudaSuccess) return e;
+  attend_fma_kernel<T, D, RT><<<tb.n_items, S::kThreads, S::kSmem, s>>>(tb, a.q, a.q_stride, a.kp, a.vp, ao,
+                                                                        scale, status);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const AttendPlan& pl, const AttendTable& tb, const AttendArgs& a,
+                         const AttendOut& ao, cudaStream_t s) {
+  const float scale = kLog2e / std::sqrt((float)D);
+  uint32_t* status = reinterpret_cast<uint32_t*>(a.ws);
+  cudaError_t e = tb.rows == 16 ? launch_fma<T, D, 2>(tb, a, ao, scale, status, s)
+                                : launch_fma<T, D, 8>(tb, a, ao, scale, status, s);
+  if (e != cudaSuccess || pl.n_merge_rows == 0) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((pl.n_merge_rows + 3) / 4));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D>, tb, pl.n_merge_rows, ao);
+}
+
+}  // namespace
+
+AttendShape attend_shape(int dtype, int D, int most) {
+  (void)dtype;
+  return AttendShape{most <= 16 ? 16 : 64, D == 128 ? 32 : 64, most <= 16 ? 4 * 148 : 2 * 148};
+}
+
+cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
+  AttendTable tb;
+  tb.n_seq = pl.n_seq; tb.n_items = pl.n_items; tb.hkv = pl.hkv; tb.g_shift = log2_of(pl.G); tb.rows = pl.rows;
+  std::copy(pl.seq, pl.seq + pl.n_seq, tb.seq);
+  const AttendOut ao{a.out, a.lse, reinterpret_cast<float2*>(a.ws + pl.off_ml),
+                     reinterpret_cast<float*>(a.ws + pl.off_o), a.out_stride, pl.Hq};
+  if (pl.dtype == WI_BF16)
+    return pl.D == 128 ? launch_typed<__nv_bfloat16, 128>(pl, tb, a, ao, s)
+                       : launch_typed<__nv_bfloat16, 64>(pl, tb, a, ao, s);
+  return pl.D == 128 ? launch_typed<float, 128>(pl, tb, a, ao, s) : launch_typed<float, 64>(pl, tb, a, ao, s);
+}
+
+}  // namespace wi

@@ -1,0 +1,386 @@
+"""The serving calls on the GPU against their plain 64-bit forms: page plans
+and appends exactly, attention within the bounds of its arithmetic
+(serve_harness.attend_bounds), and all of them together with the index build
+and decode."""
+import numpy as np
+import pytest
+import torch
+
+import retrieval_sparse_attention_wave_b200 as W
+from tests import serve_harness as S
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------- page plans
+
+def make_table(have, page, n_pages, max_pages, seed):
+    """A table whose requests hold pages for `have` tokens, and the other pages
+    on the stack in a shuffled order (with stale entries behind its end)."""
+    rng = np.random.default_rng(seed)
+    order = rng.permutation(n_pages).astype(np.int32)
+    bt = np.full((len(have), max_pages), -1, dtype=np.int32)
+    at = 0
+    for b, h in enumerate(have):
+        n = -(-h // page)
+        bt[b, :n] = order[at:at + n]
+        at += n
+    free = order[at:]
+    stack = np.concatenate([free, order[:2]])
+    return W.PageTable(i32(bt), i32(have), i32(stack), i32([len(free)]), page, n_pages)
+
+
+def check_plan(table, new, capacity, **kw):
+    bt = table.block_table.tolist()
+    ref = S.plan_reference(bt, table.seq_lens.tolist(), new, table.free_pages.tolist(),
+                           int(table.n_free), table.page_size, table.n_pages, capacity)
+    p = W.plan_pages(table, i32(new), capacity, **kw)
+    got = [x.tolist() for x in (table.block_table, p.slot_map, p.positions, p.starts, p.seq_lens)]
+    for name, a, b in zip(("table", "slots", "positions", "starts", "lens"), got, ref):
+        assert a == b, name
+    assert int(p.n_free) == ref[5]
+    return p
+
+
+@pytest.mark.parametrize("page", [1, 4, 16, 1024])
+@pytest.mark.parametrize("have,new", [
+    ([0], [1]), ([0], [0]), ([15], [1]), ([16], [1]), ([17, 0, 31, 5], [1, 40, 1, 0]),
+    ([0, 0, 0], [0, 700, 0]), ([1000, 3], [5000, 2999]),
+])
+def test_plan(page, have, new):
+    need = sum(-(-(h + n) // page) for h, n in zip(have, new))
+    table = make_table(have, page, need + 4, max(-(-(h + n) // page) for h, n in zip(have, new)) + 1, 1)
+    ws = W.serve_workspace(DEV)
+    for pad in (0, 3):
+        check_plan(table, new, sum(new) + pad, ws=ws)
+        table.block_table.copy_(make_table(have, page, need + 4, table.block_table.shape[1], 1).block_table)
+    assert W.read_device_status(ws) == 0
+
+
+def test_plan_full_batch_advances_in_place():
+    rng = np.random.default_rng(3)
+    have = rng.integers(0, 200, 256).tolist()
+    table = make_table(have, 16, 9000, 60, 4)
+    ws = W.serve_workspace(DEV)
+    for step in range(4):
+        new = (rng.integers(0, 2, 256) * (rng.integers(1, 120, 256) if step == 1 else 1)).tolist()
+        before = table.seq_lens.tolist()
+        check_plan(table, new, sum(new) + 700, update=True, ws=ws)
+        assert table.seq_lens.tolist() == [h + n for h, n in zip(before, new)]
+    assert W.read_device_status(ws) == 0
+
+
+def test_plan_captured_step_advances_with_each_replay():
+    table = make_table([30, 0, 17], 16, 40, 8, 5)
+    new = i32([1, 1, 0])
+    plan = W.PagePlan.empty(table, 4, update=True)
+    ws = W.serve_workspace(DEV)
+    ref_table = table.block_table.tolist()
+    lens, stack, n_free = table.seq_lens.tolist(), table.free_pages.tolist(), int(table.n_free)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        W.plan_pages(table, new, 4, out=plan, update=True, ws=ws)
+    assert table.seq_lens.tolist() == lens
+    for _ in range(20):
+        ref_table, slots, positions, _, lens, n_free = S.plan_reference(
+            ref_table, lens, [1, 1, 0], stack, n_free, 16, 40, 4)
+        g.replay()
+        assert plan.slot_map.tolist() == slots and plan.positions.tolist() == positions
+        assert table.seq_lens.tolist() == lens and int(table.n_free) == n_free
+    assert table.block_table.tolist() == ref_table
+    assert W.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("what,flag", [
+    ("pages", W.WI_DEV_NO_PAGES), ("capacity", W.WI_DEV_NO_PAGES), ("row", W.WI_DEV_NO_PAGES),
+    ("negative", W.WI_DEV_BAD_SLOT), ("overflow", W.WI_DEV_BAD_SLOT), ("stack", W.WI_DEV_BAD_PAGE),
+])
+def test_plan_that_does_not_fit_changes_nothing(what, flag):
+    have, new, capacity = [20, 5, 0], [30, 1, 2000], 2031
+    table = make_table(have, 16, 140, 126, 6)
+    if what == "pages":
+        table.n_free.fill_(126)         # 2 + 125 are needed
+    elif what == "capacity":
+        capacity = 2030
+    elif what == "row":
+        table.block_table = table.block_table[:, :124].contiguous()
+    elif what == "negative":
+        new = [30, -1, 2000]
+    elif what == "overflow":
+        new = [30, 1, 2 ** 31 - 1]
+        table.seq_lens[2] = 1
+    elif what == "stack":
+        table.n_free.fill_(table.free_pages.numel() + 1)
+    before = (table.block_table.tolist(), table.seq_lens.tolist(), int(table.n_free))
+    ws = W.serve_workspace(DEV)
+    p = W.plan_pages(table, i32(new), capacity, update=True, ws=ws)
+    assert W.read_device_status(ws) & flag
+    assert (table.block_table.tolist(), table.seq_lens.tolist(), int(table.n_free)) == before
+    assert set(p.slot_map.tolist()) == set(p.positions.tolist()) == {-1}
+    assert p.starts.tolist() == [0] * 4
+    # and the workspace serves the next step
+    if what == "capacity":
+        check_plan(table, new, 2031, ws=ws)
+        assert W.read_device_status(ws) == 0
+
+
+def test_plan_page_outside_the_pool():
+    table = make_table([16, 16], 16, 20, 8, 7)
+    table.free_pages[int(table.n_free) - 1] = 20       # request 0's first new page
+    table.block_table[1, 0] = -3                       # a full page: not read
+    ws = W.serve_workspace(DEV)
+    p = check_plan(table, [17, 1], 18, ws=ws)
+    assert p.slot_map.tolist()[:16] == [-1] * 16 and min(p.slot_map.tolist()[16:]) >= 0
+    assert W.read_device_status(ws) == W.WI_DEV_BAD_PAGE
+
+
+# ---------------------------------------------------------------- appends
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,d,page,n", [(1, 64, 1, 1), (8, 128, 16, 37), (3, 64, 64, 300), (2, 128, 8, 4099)])
+@pytest.mark.parametrize("fused", [False, True])
+def test_append(dtype, H, d, page, n, fused):
+    g = torch.Generator(device=DEV).manual_seed(n)
+    n_pages = n // page + 7
+    rows = torch.randn(n, 2 * H * d + (3 * H * d if fused else 0), generator=g, device=DEV).to(dtype)
+    k = rows[:, -2 * H * d:-H * d].view(n, H, d)
+    v = rows[:, -H * d:].view(n, H, d)
+    if not fused:
+        k, v = k.contiguous(), v.contiguous()
+    slots = torch.randperm(n_pages * page, generator=g, device=DEV)[:n].to(torch.int32)
+    slots[::5] = -1
+    pools = torch.randn(2, n_pages, H, page, d, generator=g, device=DEV).to(dtype)
+    want = pools.clone()
+    for i, s in enumerate(slots.tolist()):
+        if s >= 0:
+            want[0, s // page, :, s % page], want[1, s // page, :, s % page] = k[i], v[i]
+    ws = W.serve_workspace(DEV)
+    W.append_kv(k, v, slots, pools[0], pools[1], ws=ws)
+    assert torch.equal(pools, want) and W.read_device_status(ws) == 0
+
+
+def test_append_slot_outside_the_pool_is_skipped():
+    pools = torch.zeros(2, 4, 2, 16, 64, device=DEV)
+    k = torch.ones(3, 2, 64, device=DEV)
+    ws = W.serve_workspace(DEV)
+    W.append_kv(k, k, i32([64, 5, 2 ** 31 - 1]), pools[0], pools[1], ws=ws)
+    assert W.read_device_status(ws) == W.WI_DEV_BAD_SLOT
+    assert pools.sum() == 2 * 2 * 64 and (pools[:, 0, :, 5] == 1).all()
+    W.append_kv(k[:0], k[:0], i32([]), pools[0], pools[1], ws=ws)
+
+
+# -------------------------------------------------------------- attention
+
+def make_cache(lens, H, d, page, dtype, seed, stale=float("nan"), spread=1.0):
+    """A shuffled paged cache; every pool row that no token has is `stale`."""
+    g = torch.Generator().manual_seed(seed)
+    bt, n_pages = S.random_table(lens, page, seed)
+    pools = torch.full((2, n_pages, H, page, d), stale, dtype=dtype)
+    for b, T in enumerate(lens):
+        pos = torch.arange(T)
+        pages = bt[b].long()[pos // page]
+        pools[0, pages, :, pos % page] = (spread * torch.randn(T, H, d, generator=g)).to(dtype)
+        pools[1, pages, :, pos % page] = torch.randn(T, H, d, generator=g).to(dtype)
+    pools = pools.to(DEV)
+    return W.KVCache(pools[0], pools[1], bt.to(DEV), list(lens))
+
+
+def make_q(n, Hq, d, dtype, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed + 1000)
+    return (spread * torch.randn(n, Hq, d, generator=g)).to(dtype).to(DEV)
+
+
+def check_attend(kv, q, q_lens, **kw):
+    lens = kv.seq_lens
+    q_lens = lens if q_lens is None else q_lens
+    params = W.AttendParams(q.shape[1], q_lens)
+    ws = kw.pop("ws", None)
+    ws = W.attend_workspace(kv, params) if ws is None else ws
+    out, lse = W.attend(q, kv, params, ws=ws, **kw)
+    torch.cuda.synchronize()
+    assert W.read_device_status(ws) == 0
+    ref = S.attend_reference(q, kv.k_pool, kv.v_pool, kv.block_table, lens, q_lens)
+    S.assert_attend(out, lse, ref, q.dtype, max(lens), q.shape[2])
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_attend_ragged_prompts(dtype, d, G):
+    kv = make_cache([1, 17, 130, 64, 300, 257], 2, d, 16, dtype, G)
+    check_attend(kv, make_q(769, 2 * G, d, dtype, G), None)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 32, 128, 1024])
+def test_attend_page_sizes(dtype, page):
+    kv = make_cache([333, 40, 129], 2, 128, page, dtype, page)
+    check_attend(kv, make_q(333 + 7, 4, 128, dtype, 1), [333, 0, 7])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens,q_lens", [
+    ([1], [1]), ([128], [1]), ([129], [1]), ([5000], [1]), ([3000, 1, 777], [1, 1, 1]),
+    ([2500], [3]), ([2500, 900], [33, 900]), ([1025, 1024, 1023], [65, 64, 63]),
+    ([600, 600, 600], [0, 600, 0]), ([4000, 200], [0, 1]),
+])
+@pytest.mark.parametrize("H,G,d", [(1, 8, 128), (2, 1, 64), (4, 4, 128)])
+def test_attend_chunks_and_single_tokens(dtype, lens, q_lens, H, G, d):
+    kv = make_cache(lens, H, d, 16, dtype, sum(lens))
+    check_attend(kv, make_q(sum(q_lens), H * G, d, dtype, 2), q_lens)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("q_len", [1, 260])
+def test_attend_large_scores_rising_along_the_keys(dtype, q_len):
+    """Scores over hundreds: a weight is 0 or all of it, and the running
+    maximum rises again and again."""
+    kv = make_cache([900], 1, 64, 16, dtype, 9, spread=6.0)
+    pages = kv.block_table[0].long()[torch.arange(900, device=DEV) // 16]
+    ramp = torch.linspace(0.1, 3.0, 900, device=DEV)[:, None, None]
+    rows = torch.arange(900, device=DEV) % 16
+    kv.k_pool[pages, :, rows] = (kv.k_pool[pages, :, rows].float().abs() * ramp).to(dtype)
+    check_attend(kv, make_q(q_len, 4, 64, dtype, 3, spread=3.0).abs(), [q_len])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_strided_rows_and_rows_behind_the_last_sequence(dtype):
+    lens, H, G, d, n = [70, 333], 2, 4, 128, 403
+    kv = make_cache(lens, H, d, 16, dtype, 11)
+    wide = make_q(n + 9, H * G + 2 * H, d, dtype, 4)
+    q = wide[:, :H * G]
+    into = torch.full((n + 9, H * G + 3, d), 7.0, dtype=dtype, device=DEV)
+    lse = torch.full((n + 9, H * G), 7.0, device=DEV)
+    out, _ = check_attend(kv, q, None, out=into[:, 2:2 + H * G], lse=lse)
+    assert (into[n:] == 7).all() and (into[:, :2] == 7).all() and (into[:, -1] == 7).all()
+    assert (lse[n:] == 7).all()
+    plain, _ = W.attend(q[:n].contiguous(), kv, W.AttendParams(H * G))
+    assert torch.equal(plain, out[:n])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens,q_lens", [([300], [300]), ([1500], [40])])
+def test_attend_later_keys_have_no_effect(dtype, bad, lens, q_lens):
+    """A key or value that is not finite reaches the queries behind it, and
+    only those."""
+    T, n = lens[0], q_lens[0]
+    kv = make_cache(lens, 2, 128, 16, dtype, 13)
+    q = make_q(n, 8, 128, dtype, 5)
+    clean, clean_lse = W.attend(q, kv, W.AttendParams(8, q_lens))
+    at = T - n // 2                     # a position half way through the queries
+    i = at - (T - n)
+    page, row = int(kv.block_table[0, at // 16]), at % 16
+    kv.v_pool[page, 0, row, 5] = bad
+    kv.k_pool[page, 1, row, :] = bad
+    out, lse = W.attend(q, kv, W.AttendParams(8, q_lens))
+    assert torch.equal(out[:i], clean[:i]) and torch.equal(lse[:i], clean_lse[:i])
+    hit = out[i:, :4, 5]
+    assert (hit == bad).all() if bad == bad else torch.isnan(hit).all()
+    rest = [c for c in range(128) if c != 5]
+    assert torch.equal(out[:, :4, rest], clean[:, :4, rest])      # the other channels
+    assert torch.equal(lse[:, :4], clean_lse[:, :4])
+    if bad != bad:
+        assert torch.isnan(out[i:, 4:]).all() and torch.isnan(lse[i:, 4:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_page_outside_the_pool_is_flagged(dtype):
+    kv = make_cache([300, 120], 2, 128, 16, dtype, 15)
+    q = make_q(420, 4, 128, dtype, 6)
+    params = W.AttendParams(4)
+    ws = W.attend_workspace(kv, params)
+    clean, _ = W.attend(q, kv, params, ws=ws)
+    for wrong in (-1, kv.k_pool.shape[0], 2 ** 31 - 1):
+        kv.block_table[0, 18] = wrong              # positions 288..299
+        out, _ = W.attend(q, kv, params, ws=ws)
+        assert W.read_device_status(ws) == W.WI_DEV_BAD_PAGE
+        assert torch.equal(out[:288], clean[:288]) and torch.equal(out[300:], clean[300:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_repeats_bit_for_bit_on_a_used_workspace(dtype):
+    kv = make_cache([5000, 310], 2, 128, 16, dtype, 17)
+    q = make_q(2, 8, 128, dtype, 7)
+    params = W.AttendParams(8, [1, 1])
+    first, first_lse = check_attend(kv, q, [1, 1])
+    big = W.workspace(1 << 24, DEV)
+    big[256:].fill_(255)                           # what another call left
+    for _ in range(2):
+        out, lse = W.attend(q, kv, params, ws=big)
+        assert torch.equal(out, first) and torch.equal(lse, first_lse)
+
+
+def test_attend_on_another_stream_and_captured():
+    kv = make_cache([2000, 77], 2, 128, 16, BF16, 19)
+    params = W.AttendParams(8, [1, 77])
+    q = make_q(78, 8, 128, BF16, 8)
+    ref, ref_lse = check_attend(kv, q, [1, 77])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = W.attend(q, kv, params, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    ws, into, into_lse = W.attend_workspace(kv, params), torch.zeros_like(ref), torch.zeros_like(ref_lse)
+    held = q.clone()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        W.attend(held, kv, params, out=into, lse=into_lse, ws=ws)
+    for seed in (8, 9):
+        held.copy_(make_q(78, 8, 128, BF16, seed))
+        g.replay()
+        want, want_lse = W.attend(held, kv, params)
+        assert torch.equal(into, want) and torch.equal(into_lse, want_lse)
+    with pytest.raises(W.WaveIndexError):
+        W.attend(q, kv, params, ws=W.workspace(256, DEV))
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_prompt_to_decode_through_one_cache(dtype):
+    """Pages planned, a prompt's rows appended and attended, decode steps
+    planned, appended and attended, then the index built from the same cache:
+    its decode with every cluster retrieved is the same dense attention."""
+    H, G, d, page, lens = 2, 4, 128, 16, [700, 33, 260]
+    B, Hq = len(lens), H * G
+    n_pages, max_pages = 80, 60
+    table = W.PageTable.empty(B, max_pages, page, n_pages, DEV)
+    pools = torch.full((2, n_pages, H, page, d), float("nan"), dtype=dtype, device=DEV)
+    ws = W.serve_workspace(DEV)
+    have = [0] * B
+    for step, new in enumerate(([700, 20, 260], [0, 13, 0], [1, 1, 1], [1, 0, 1], [1, 1, 1])):
+        n = sum(new)
+        rows = make_q(n, Hq + 2 * H, d, dtype, 40 + step)
+        q, k, v = rows[:, :Hq], rows[:, Hq:Hq + H], rows[:, Hq + H:]
+        plan = W.plan_pages(table, i32(new), n, update=True, ws=ws)
+        W.append_kv(k, v, plan.slot_map, pools[0], pools[1], ws=ws)
+        have = [h + m for h, m in zip(have, new)]
+        assert table.seq_lens.tolist() == have
+        kv = W.KVCache(pools[0], pools[1], table.block_table, have)
+        # the rows are where the table says they are
+        for b in range(B):
+            for i in range(new[b]):
+                pos, t = have[b] - new[b] + i, int(plan.starts[b]) + i
+                if i in (0, new[b] - 1):
+                    assert torch.equal(pools[0, int(table.block_table[b, pos // page]), :, pos % page], k[t])
+        out, lse = check_attend(kv, q, new)
+    assert W.read_device_status(ws) == 0
+    idx = W.build_index(kv, 256, 16, 2)
+    dp = W.DecodeParams(n_q_heads=Hq, n_sink=4, window=16, topk_clusters=10 ** 6)
+    dec, dec_lse = W.decode(q.contiguous(), idx, dp)
+    ref = S.attend_reference(q, kv.k_pool, kv.v_pool, kv.block_table, have, new)
+    tol_out, tol_lse = S.attend_bounds(*ref, dtype, max(have), d)
+    gap = (dec.double() - out.double()).abs().cpu().numpy()
+    # decode's own bound against dense attention is 2e-4 (bf16) or 1e-5 (fp32) of rms / max
+    assert (gap <= tol_out + 2e-4 * np.abs(ref[0]).max()).all()
+    assert (np.abs(dec_lse.cpu().numpy() - lse.cpu().numpy()) <= tol_lse + 1e-4).all()
