@@ -12,68 +12,17 @@
 #include <atomic>
 #include <cmath>
 
-#include "wi_serve.h"
+#include "wi_attend.cuh"
 
 namespace wi {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct AttendTable {
-  int32_t n_seq, n_items, hkv, g_shift, rows;
-  AttendSeq seq[kMaxBatch];
-};
-
-// One item of the plan, as its CTA needs it.
-struct Item {
-  int b, h, T, n, q0;
-  int row0, rows;       // its rows of the unit
-  int pos0;             // position of query token 0 of the sequence
-  int key_end;          // keys its last row sees
-  int t0, t1;           // key tiles
-  int64_t part;         // first part row, -1: the whole key range
-};
-
-__device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT) {
-  int lo = 0, hi = tb.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tb.seq[mid].item0 <= item) lo = mid; else hi = mid - 1;
-  }
-  const AttendSeq& s = tb.seq[lo];
-  Item it;
-  const int x = item - s.item0, split = x % s.ns, y = x / s.ns;
-  const int blk = s.nblk - 1 - y / tb.hkv, all = s.n << tb.g_shift;
-  it.h = y % tb.hkv;
-  it.b = s.b; it.T = s.T; it.n = s.n; it.q0 = s.q0;
-  it.row0 = blk * tb.rows;
-  it.rows = min(tb.rows, all - it.row0);
-  it.pos0 = s.T - s.n;
-  it.key_end = it.pos0 + ((it.row0 + it.rows - 1) >> tb.g_shift) + 1;
-  const int64_t nt = (it.key_end + KT - 1) / KT;
-  it.t0 = (int)(nt * split / s.ns);
-  it.t1 = (int)(nt * (split + 1) / s.ns);
-  it.part = -1;
-  if (s.ns > 1)
-    it.part = s.part0 + (((int64_t)blk * tb.hkv + it.h) * s.ns + split) * min(tb.rows, all);
-  return it;
-}
-
-struct AttendOut {
-  void* out;
-  float* lse;
-  float2* ml;
-  float* o;
-  int64_t stride;
-  int Hq;
-};
-
-// ------------------------------------------------------------ FMA kernel
+// ------------------------------------------------- fp32, on packed FMAs
 // 128 threads, 16 of them (half a warp) share a row group of RT rows: each
 // takes every 16th key of a tile and every 16th 16-byte chunk of the output
 // columns, so a row's statistics and weights stay inside its half warp.
 // Products run on packed fp32 FMAs (two head channels at a time).
-template <typename T, int D, int RT>
+template <int D, int RT>
 struct FmaShape {
   static constexpr int kThreads = 128;
   static constexpr int R = 8 * RT;
@@ -85,11 +34,11 @@ struct FmaShape {
   static constexpr size_t kSmem = (size_t)(R * LD + 2 * KT * LD + R * PLD) * 4;
 };
 
-template <typename T, int D, int RT>
+template <int D, int RT>
 __global__ void __launch_bounds__(128)
-attend_fma_kernel(const __grid_constant__ AttendTable tb, const void* __restrict__ q_, int64_t q_stride,
+attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restrict__ q_, int64_t q_stride,
                   const Pool kp, const Pool vp, const AttendOut ao, float scale, uint32_t* status) {
-  using S = FmaShape<T, D, RT>;
+  using S = FmaShape<D, RT>;
   extern __shared__ __align__(16) float sh_fma[];
   float* sq = sh_fma;
   float* sk = sq + S::R * S::LD;
@@ -99,26 +48,16 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const void* __restrict
   pdl_launch_dependents();
   const Item it = item_of(tb, blockIdx.x, S::KT);
   const int G = 1 << tb.g_shift;
-  constexpr int VE = Elem<T>::kPerVec, CH = D / VE;
+  constexpr int CH = D / 4;   // 16-byte chunks of a row
 
   // rows [base, base + KT) of a pool into a tile; rows behind key_end are zero
   auto load_tile = [&](const Pool& p, float* dst, int base) {
     for (int c = tid; c < S::KT * CH; c += 128) {
       const int r = c / CH, ch = c % CH;
       const int64_t row = base + r < it.key_end ? pool_row(p, tb.hkv, D, it.b, it.h, base + r, status) : -1;
-      float* to = dst + r * S::LD + ch * VE;
-      const T* from = reinterpret_cast<const T*>(p.base) + row + ch * VE;
-      if (row < 0) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) to[e] = 0.f;
-      } else if constexpr (sizeof(T) == 4) {
-        cp_async16(to, from);
-      } else {
-        float x[VE];
-        Elem<T>::unpack(ld_stream(from), x);
-#pragma unroll
-        for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-      }
+      float* to = dst + r * S::LD + ch * 4;
+      if (row >= 0) cp_async16(to, reinterpret_cast<const float*>(p.base) + row + ch * 4);
+      else *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     cp_async_commit();
   };
@@ -126,17 +65,13 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const void* __restrict
   if (it.t0 < it.t1) load_tile(kp, sk, it.t0 * S::KT);
   for (int c = tid; c < S::R * CH; c += 128) {
     const int r = c / CH, ch = c % CH;
-    float x[VE];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) x[e] = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < it.rows) {
       const int row = it.row0 + r;
-      const T* from = reinterpret_cast<const T*>(q_) + (int64_t)(it.q0 + (row >> tb.g_shift)) * q_stride +
-                      (int64_t)(it.h * G + (row & (G - 1))) * D + ch * VE;
-      Elem<T>::unpack(ld_stream(from), x);
+      x = *reinterpret_cast<const float4*>(q_ + (int64_t)(it.q0 + (row >> tb.g_shift)) * q_stride +
+                                           (int64_t)(it.h * G + (row & (G - 1))) * D + ch * 4);
     }
-#pragma unroll
-    for (int e = 0; e < VE; ++e) sq[r * S::LD + ch * VE + e] = x[e] * scale;
+    *reinterpret_cast<float4*>(sq + r * S::LD + ch * 4) = make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
   }
   float m[RT], l[RT];
   float4 o[RT][S::CPT];
@@ -266,14 +201,12 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const void* __restrict
       const int64_t tok = it.q0 + (row >> tb.g_shift);
       const int head = it.h * G + (row & (G - 1));
       if (tx == 0 && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m[i] + log2f(l[i]));
-      T* to = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D;
+      float* to = reinterpret_cast<float*>(ao.out) + tok * ao.stride + (int64_t)head * D;
       const float inv = 1.f / l[i];
 #pragma unroll
-      for (int cc = 0; cc < S::CPT; ++cc) {
-        const float4 x = make_float4(o[i][cc].x * inv, o[i][cc].y * inv, o[i][cc].z * inv, o[i][cc].w * inv);
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to + 4 * (tx + 16 * cc)) = x;
-        else *reinterpret_cast<uint2*>(to + 4 * (tx + 16 * cc)) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-      }
+      for (int cc = 0; cc < S::CPT; ++cc)
+        *reinterpret_cast<float4*>(to + 4 * (tx + 16 * cc)) =
+            make_float4(o[i][cc].x * inv, o[i][cc].y * inv, o[i][cc].z * inv, o[i][cc].w * inv);
     }
   }
 }
@@ -342,43 +275,23 @@ attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const At
   for (int e = 0; e < E; ++e) store_elem(to + e, o[e] * inv);
 }
 
-int log2_of(int x) { int r = 0; while ((1 << r) < x) ++r; return r; }
+inline int log2_of(int x) { int r = 0; while ((1 << r) < x) ++r; return r; }
 
-// Dynamic shared memory limit of a kernel, raised once per device.
-template <auto kern>
-cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> done{0};   // one bit per device (the first 64)
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+template <int D, int RT>
+cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendOut& ao, cudaStream_t s) {
+  using S = FmaShape<D, RT>;
+  const cudaError_t e = allow_smem<attend_fma_kernel<D, RT>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
-template <typename T, int D, int RT>
-cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendOut& ao, float scale,
-                       uint32_t* status, cudaStream_t s) {
-  using S = FmaShape<T, D, RT>;
-  const cudaError_t e = allow_smem<attend_fma_kernel<T, D, RT>>(S::kSmem);
-  if (e != cudaSuccess) return e;
-  attend_fma_kernel<T, D, RT><<<tb.n_items, S::kThreads, S::kSmem, s>>>(tb, a.q, a.q_stride, a.kp, a.vp, ao,
-                                                                        scale, status);
+  attend_fma_kernel<D, RT><<<tb.n_items, S::kThreads, S::kSmem, s>>>(
+      tb, static_cast<const float*>(a.q), a.q_stride, a.kp, a.vp, ao, kLog2e / std::sqrt((float)D),
+      reinterpret_cast<uint32_t*>(a.ws));
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AttendPlan& pl, const AttendTable& tb, const AttendArgs& a,
-                         const AttendOut& ao, cudaStream_t s) {
-  const float scale = kLog2e / std::sqrt((float)D);
-  uint32_t* status = reinterpret_cast<uint32_t*>(a.ws);
-  cudaError_t e = tb.rows == 16 ? launch_fma<T, D, 2>(tb, a, ao, scale, status, s)
-                                : launch_fma<T, D, 8>(tb, a, ao, scale, status, s);
-  if (e != cudaSuccess || pl.n_merge_rows == 0) return e;
+cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((pl.n_merge_rows + 3) / 4));
+  cfg.gridDim = dim3((unsigned)((n_rows + 3) / 4));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -386,13 +299,15 @@ cudaError_t launch_typed(const AttendPlan& pl, const AttendTable& tb, const Atte
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D>, tb, pl.n_merge_rows, ao);
+  return cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D>, tb, n_rows, ao);
 }
 
 }  // namespace
 
+// bf16: 256 rows a block where some sequence has more than a tile of 128.
+// fp32: 64 rows, or 16 where no block has more to fill.
 AttendShape attend_shape(int dtype, int D, int most) {
-  (void)dtype;
+  if (dtype == WI_BF16) return AttendShape{most <= 128 ? 128 : 256, 128, 148};
   return AttendShape{most <= 16 ? 16 : 64, D == 128 ? 32 : 64, most <= 16 ? 4 * 148 : 2 * 148};
 }
 
@@ -402,10 +317,17 @@ cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_
   std::copy(pl.seq, pl.seq + pl.n_seq, tb.seq);
   const AttendOut ao{a.out, a.lse, reinterpret_cast<float2*>(a.ws + pl.off_ml),
                      reinterpret_cast<float*>(a.ws + pl.off_o), a.out_stride, pl.Hq};
+  const bool wide = pl.D == 128;
+  cudaError_t e;
+  if (pl.dtype == WI_BF16) e = launch_attend_umma(tb, pl, a, ao, s);
+  else if (pl.rows == 16) e = wide ? launch_fma<128, 2>(tb, a, ao, s) : launch_fma<64, 2>(tb, a, ao, s);
+  else e = wide ? launch_fma<128, 8>(tb, a, ao, s) : launch_fma<64, 8>(tb, a, ao, s);
+  if (e != cudaSuccess || pl.n_merge_rows == 0) return e;
   if (pl.dtype == WI_BF16)
-    return pl.D == 128 ? launch_typed<__nv_bfloat16, 128>(pl, tb, a, ao, s)
-                       : launch_typed<__nv_bfloat16, 64>(pl, tb, a, ao, s);
-  return pl.D == 128 ? launch_typed<float, 128>(pl, tb, a, ao, s) : launch_typed<float, 64>(pl, tb, a, ao, s);
+    return wide ? launch_merge<__nv_bfloat16, 128>(tb, pl.n_merge_rows, ao, s)
+                : launch_merge<__nv_bfloat16, 64>(tb, pl.n_merge_rows, ao, s);
+  return wide ? launch_merge<float, 128>(tb, pl.n_merge_rows, ao, s)
+              : launch_merge<float, 64>(tb, pl.n_merge_rows, ao, s);
 }
 
 }  // namespace wi
