@@ -38,6 +38,9 @@ namespace {
 constexpr int kRows = 128;          // rows of a query tile, keys of a key tile
 constexpr int kUThreads = 384;
 constexpr float kRescale = 8.f;     // log2 of the growth that forces a rescale
+constexpr int kPoly = 4;            // every kPoly-th pair of weights without the special-function unit
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kUThreads * 168, "within the launch's registers");
 
 template <int D>
 struct UmmaShape {
@@ -62,6 +65,36 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^x without the special-function unit: x = n + f, |f| <= 1/2 (the sum with
+// 1.5 * 2^23 rounds x to the integer n, which is then in its low bits), 2^f
+// from a degree-5 polynomial (value 1 at 0, the others fitted for the least
+// largest relative error, 2^-22.6 in fp32), n added to the exponent.  From
+// -127 down the result is 0 (n = -127, f = 0).
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  const auto two = [](float v) { return make_float2(v, v); };
+  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  const float2 t = __fadd2_rn(x, two(12582912.f));
+  const float2 f = __ffma2_rn(__fadd2_rn(t, two(-12582912.f)), two(-1.f), x);
+  float2 p = __ffma2_rn(f, two(0x1.5bba14p-10f), two(0x1.3cea88p-7f));
+  p = __ffma2_rn(p, f, two(0x1.c6b752p-5f));
+  p = __ffma2_rn(p, f, two(0x1.ebf9bcp-3f));
+  p = __ffma2_rn(p, f, two(0x1.62e42ap-1f));
+  p = __ffma2_rn(p, f, two(1.f));
+  return make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + __float_as_uint(p.x)),
+                     __uint_as_float((__float_as_uint(t.y) << 23) + __float_as_uint(p.y)));
+}
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// the largest of three, NaN if one is NaN
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kUThreads, 1)
@@ -74,9 +107,10 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   unsigned char* sq = align_smem_1024(sh_raw);
   unsigned char* ring = sq + 2 * S::kTile;
   __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
-  __shared__ __align__(8) uint64_t s_q, s_s[2], s_p[2], s_o[2], s_go, s_fixed, s_done;
+  __shared__ __align__(8) uint64_t s_q, s_s[2], s_p[2][2], s_o[2], s_go, s_fixed, s_done;
   __shared__ uint32_t s_tmem, s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler)
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -86,7 +120,8 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
     mbar_init(&s_q, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_s[i], 1);
-      mbar_init(&s_p[i], 4);
+      mbar_init(&s_p[i][0], 4);
+      mbar_init(&s_p[i][1], 4);
       mbar_init(&s_o[i], 1);
     }
     mbar_init(&s_go, 1);
@@ -99,7 +134,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
 
   const Item it = item_of(tb, blockIdx.x, kRows);
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
@@ -108,6 +143,8 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   // a key tile on the diagonal: some row of the block does not see all of it
   auto diagonal = [&](int t) { return t * kRows + kRows - 1 > first_pos; };
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8 && n > 0) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
@@ -192,56 +229,77 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
     }
   } else if (warp == 9 && n > 0) {
     // ----------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = umma_idesc_bf16_f32<128, 128>();
-      constexpr uint32_t kIdescO = umma_idesc_bf16_f32<128, D>() | kIdescBMn;
-      const uint32_t q_addr = smem_addr(sq), r_addr = smem_addr(ring);
-      auto scores = [&](int i, int st) {   // S_i = Q_i K^T
-        const uint32_t a = q_addr + i * S::kTile, b = r_addr + st * S::kTile;
+    // The whole warp runs the loop, so that addresses and descriptors stay in
+    // uniform registers; one elected lane issues each batch.
+    constexpr uint32_t kIdescS = umma_idesc_bf16_f32<128, 128>();
+    constexpr uint32_t kIdescO = umma_idesc_bf16_f32<128, D>() | kIdescBMn;
+    constexpr uint64_t kStep = S::kTile >> 4;   // a stage, in descriptor units
+    const uint64_t dq = umma_desc_sw128(smem_addr(sq)), dk = umma_desc_sw128(smem_addr(ring));
+    const uint64_t dv = umma_desc_sw128_mn(smem_addr(ring), S::kBlock);
+    auto scores = [&](int i, int st, bool last) {   // S_i = Q_i K^T
+      if (elect_one()) {
+        const uint64_t a = dq + i * kStep, b = dk + st * kStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t ko = (uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u;
-          umma_bf16(tmem + S::kS + i * 128, umma_desc_sw128(a + ko), umma_desc_sw128(b + ko), kIdescS, k != 0);
+          const uint32_t ko = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u) >> 4;
+          umma_bf16(tmem + S::kS + i * 128, a + ko, b + ko, kIdescS, k != 0);
         }
         umma_commit(&s_s[i]);
-      };
-      auto full = [&](int u) { return mbar_wait(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status); };
-      bool ok = mbar_wait(&s_q, 0, status) && full(0);
-      tc_fence_after();
-      if (ok) {
-        for (int i = 0; i < nq; ++i) scores(i, 0);
-        umma_commit(&s_empty[0]);
+        if (last) umma_commit(&s_empty[st]);
       }
-      int fixes = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int v = 2 * j + 1, k = v + 1;
-        const bool fix = diagonal(it.t0 + j);
-        if (!(ok = full(v))) break;
-        if (fix) mbar_arrive(&s_go);
-        for (int i = 0; i < nq && ok; ++i) {
-          ok = mbar_wait(&s_p[i], (uint32_t)j & 1u, status);
-          if (ok && fix && i == 0) ok = mbar_wait(&s_fixed, (uint32_t)fixes++ & 1u, status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t b = r_addr + (v % S::kStages) * S::kTile;
+      __syncwarp();
+    };
+    auto output = [&](int i, int st, int half, bool first) {   // O_i += P_i V, half of the keys
+      if (elect_one()) {
+        const uint64_t b = dv + st * kStep;
 #pragma unroll
-          for (int kk = 0; kk < kRows / 16; ++kk)   // O_i += P_i V
-            umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + kk * 8,
-                         umma_desc_sw128_mn(b + kk * 2048, S::kBlock), kIdescO, (j | kk) != 0);
+        for (int kk = 0; kk < kRows / 32; ++kk) {
+          const int k = half * (kRows / 32) + kk;
+          umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
+                       !first || kk != 0);
+        }
+        if (half == 1) {
           umma_commit(&s_o[i]);
-          if (i == nq - 1) umma_commit(&s_empty[v % S::kStages]);
-          if (j + 1 < n) {
-            if (i == 0 && !(ok = full(k))) break;
-            tc_fence_after();
-            scores(i, k % S::kStages);
-            if (i == nq - 1) umma_commit(&s_empty[k % S::kStages]);
-          }
+          if (i == nq - 1) umma_commit(&s_empty[st]);
         }
       }
-      // every MMA issued has completed before the columns are released
-      umma_commit(&s_done);
-      mbar_wait(&s_done, 0, status);
+      __syncwarp();
+    };
+    // a ring position: unit u in stage st, phase ph
+    auto full = [&](int st, uint32_t ph) { return mbar_wait(&s_full[st], ph, status); };
+    bool ok = mbar_wait(&s_q, 0, status) && full(0, 0);
+    tc_fence_after();
+    if (ok)
+      for (int i = 0; i < nq; ++i) scores(i, 0, i == nq - 1);
+    int fixes = 0, st = 1;
+    uint32_t ph = 0;
+    for (int j = 0; j < n && ok; ++j) {
+      const bool fix = diagonal(it.t0 + j);
+      if (!(ok = full(st, ph))) break;   // V_j
+      if (fix && lane == 0) mbar_arrive(&s_go);
+      const int sv = st;
+      if (++st == S::kStages) { st = 0; ph ^= 1; }
+      for (int i = 0; i < nq && ok; ++i) {
+        ok = mbar_wait(&s_p[i][0], (uint32_t)j & 1u, status);
+        if (ok && fix && i == 0) ok = mbar_wait(&s_fixed, (uint32_t)fixes++ & 1u, status);
+        if (!ok) break;
+        tc_fence_after();
+        output(i, sv, 0, j == 0);
+        if (!(ok = mbar_wait(&s_p[i][1], (uint32_t)j & 1u, status))) break;
+        tc_fence_after();
+        output(i, sv, 1, false);
+        if (j + 1 < n) {
+          if (i == 0 && !(ok = full(st, ph))) break;   // K_(j + 1)
+          tc_fence_after();
+          scores(i, st, i == nq - 1);
+        }
+      }
+      if (++st == S::kStages) { st = 0; ph ^= 1; }
     }
+    // every MMA issued has completed before the columns are released
+    if (elect_one()) umma_commit(&s_done);
+    __syncwarp();
+    mbar_wait(&s_done, 0, status);
   } else if (warp >= 10 && n > 0) {
     // ------------------------------------------- value tiles on the diagonal
     int fixes = 0;
@@ -279,8 +337,10 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_fixed);
     }
-  } else if (warp < 8) {
+  }
+  } else {
     // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2, r = i * kRows + 32 * (warp & 3) + lane;
     const int pos = it.pos0 + ((it.row0 + r) >> tb.g_shift);
     const int warp_pos = __shfl_sync(0xffffffffu, pos, 0);
@@ -316,10 +376,15 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           for (int c = 0; c < 4; ++c) {
             mx[c] = __uint_as_float(x[c][0]);
 #pragma unroll
-            for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
+            for (int e = 1; e < 31; e += 2)
+              mx[c] = max3_nan(mx[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-          const bool up = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
+          mx[0] = max3_nan(mx[0], __uint_as_float(x[0][31]), __uint_as_float(x[1][31]));
+          mx[1] = max3_nan(mx[1], __uint_as_float(x[2][31]), __uint_as_float(x[3][31]));
+          // a score that is NaN or +inf makes its row NaN
+          float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale;
+          top = top < INFINITY ? top : NAN;
+          const bool up = !(top <= m + kRescale);
           if (__any_sync(0xffffffffu, up)) {
             const float mn = up ? top : m;
             const float c = up ? ex2(m - mn) : 1.f;
@@ -342,25 +407,34 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           }
           const float mu = m == -INFINITY ? 0.f : m;
           const float2 sc = make_float2(scale, scale), nm = make_float2(-mu, -mu);
-          float2 sum = make_float2(0.f, 0.f);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc, nm);
-              const float2 w = make_float2(ex2(y.x), ex2(y.y));
-              sum = __fadd2_rn(sum, w);
-              p[e / 2] = pack_bf16(w.x, w.y);
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc, nm);
+              const float2 w = e % kPoly == kPoly - 1 ? ex2_poly(y) : make_float2(ex2(y.x), ex2(y.y));
+              sum[e & 1] = __fadd2_rn(sum[e & 1], w);
+              p[e] = pack_bf16(w.x, w.y);
             }
             tmem_st16(ts + 16 * c, p);
+            if (c == 1) {   // the product over the first half may start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_p[i][0]);
+            }
           }
-          l += sum.x + sum.y;
           tmem_wait_st();
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_p[i][1]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        } else if (lane == 0) {
+          mbar_arrive(&s_p[i][0]);
+          mbar_arrive(&s_p[i][1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_p[i]);
       }
       if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_o[i], (uint32_t)(n - 1) & 1u, status));
     }
