@@ -8,7 +8,9 @@
 // Roles:
 //   warps 0..3, 4..7  softmax of query tile 0, 1: a thread owns a row
 //                     (a tensor-memory lane), so its maximum, mass and output
-//                     scale need no exchange;
+//                     scale need no exchange; a lone query tile (single
+//                     tokens, short prompts) has its key tiles taken in turns
+//                     by both;
 //   warp 8            the queries (one 3-D tensor copy a tile and 64
 //                     channels), then K_0, V_0, K_1, V_1, ... into a ring of
 //                     stages: a tensor copy per page and 64 channels;
@@ -108,6 +110,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   unsigned char* ring = sq + 2 * S::kTile;
   __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
   __shared__ __align__(8) uint64_t s_q, s_s[2], s_p[2][2], s_o[2], s_go, s_fixed, s_done;
+  __shared__ float2 s_ml[kRows];
   __shared__ uint32_t s_tmem, s_bad;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler)
@@ -138,7 +141,10 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
 
   const Item it = item_of(tb, blockIdx.x, kRows);
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
-  const int nq = it.rows > kRows ? 2 : 1;
+  // Two query tiles take every key tile each; a lone one has its key tiles
+  // taken in turns by the two softmax groups, each with its own (m, l, O).
+  const bool lone = it.rows <= kRows;
+  const int ahead = lone ? 2 : 1;   // key tiles whose scores are under way
   const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
   // a key tile on the diagonal: some row of the block does not see all of it
   auto diagonal = [&](int t) { return t * kRows + kRows - 1 > first_pos; };
@@ -148,6 +154,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   if (warp == 8 && n > 0) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
+      const int nq = lone ? 1 : 2;
       mbar_arrive_expect(&s_q, (uint32_t)nq * S::kTile);
       for (int i = 0; i < nq; ++i)
         for (int c = 0; c < S::kBlocks; ++c)
@@ -163,32 +170,41 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       const int r_shift = min(kp.page_shift, 7), per = kRows >> r_shift;
       const int bx = lane & (per - 1), c = lane / per;
       const int none = (int)((kp.n_pages * tb.hkv) << kp.page_shift);
-      auto page_at = [&](int t) {
-        const int key = t * kRows + (bx << r_shift);
-        return key < it.key_end && t < it.t1 ? __ldg(bt + (key >> kp.page_shift)) : -1;
+      auto page_at = [&](int j) {   // of this lane's box in key tile j (looked up tiles ahead of its use)
+        const int key = (it.t0 + j) * kRows + (bx << r_shift);
+        return j < n && key < it.key_end ? __ldg(bt + (key >> kp.page_shift)) : INT32_MAX;
       };
-      int page = page_at(it.t0), issued = 0;
+      auto row_at = [&](int j, int page) {
+        const int key = (it.t0 + j) * kRows + (bx << r_shift);
+        if (page >= 0 && page < kp.n_pages)
+          return ((page * tb.hkv + it.h) << kp.page_shift) + (key & page_mask);
+        if (j < n && key < it.key_end) flag_error(status, WI_DEV_BAD_PAGE);
+        return none;
+      };
+      // unit u: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead) in turns; a
+      // tile's row is kept from its keys to its values
+      int issued = 0, st = 0, page = page_at(2);
+      int y0 = row_at(0, page_at(0)), y1 = row_at(1, page_at(1));
+      uint32_t ph = 1;
+      auto load = [&](const CUtensorMap* map, int row) {
+        if (issued >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[st], ph, status));
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect(&s_full[st], S::kTile);
+        __syncwarp();
+        if (c < S::kBlocks)
+          tensor_load_2d(ring + (size_t)st * S::kTile + c * S::kBlock + (bx << r_shift) * 128, map, 64 * c, row, &s_full[st]);
+        ++issued;
+        if (++st == S::kStages) { st = 0; ph ^= 1; }
+      };
+      load(&map_k, y0);
+      if (lone && n > 1) load(&map_k, y1);
       for (int j = 0; j < n && ok; ++j) {
-        const int t = it.t0 + j, key = t * kRows + (bx << r_shift);
-        int y = none;
-        if (key < it.key_end) {
-          if (page >= 0 && page < kp.n_pages)
-            y = ((page * tb.hkv + it.h) << kp.page_shift) + (key & page_mask);
-          else
-            flag_error(status, WI_DEV_BAD_PAGE);
-        }
-        page = page_at(t + 1);
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int u = 2 * j + kv, st = u % S::kStages;
-          if (u >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect(&s_full[st], S::kTile);
-          __syncwarp();
-          if (c < S::kBlocks)
-            tensor_load_2d(ring + (size_t)st * S::kTile + c * S::kBlock + (bx << r_shift) * 128,
-                           kv ? &map_v : &map_k, 64 * c, y, &s_full[st]);
-          issued = u + 1;
-        }
+        const int y2 = row_at(j + 2, page);
+        page = page_at(j + 3);
+        load(&map_v, y0);
+        if (ok && j + ahead < n) load(&map_k, lone ? y2 : y1);
+        y0 = y1;
+        y1 = y2;
       }
       if (!ok)   // a wait gave up: no copy is left in flight when the CTA ends
         for (int u = max(0, issued - S::kStages); u < issued; ++u)
@@ -204,10 +220,15 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       };
       int u = 0;
       for (; u < 2 * n && ok; ++u) {
-        const int t = it.t0 + u / 2, st = u % S::kStages;
+        // the same order: past the first `ahead`, values at every other unit
+        // until the keys have run out
+        const int x = u - min(ahead, n), keys_left = 2 * (n - min(ahead, n));
+        const bool val = x >= 0 && ((x & 1) == 0 || x >= keys_left);
+        const int j = x < 0 ? u : x >= keys_left ? x - keys_left / 2 : val ? x / 2 : x / 2 + ahead;
+        const int t = it.t0 + j, st = u % S::kStages;
         if (u >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
         if (!ok) break;
-        const Pool& p = u & 1 ? vp : kp;
+        const Pool& p = val ? vp : kp;
         unsigned char* dst = ring + (size_t)st * S::kTile;
 #pragma unroll 4
         for (int i = lane; i < kRows * CH; i += 32) {
@@ -238,7 +259,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
     const uint64_t dv = umma_desc_sw128_mn(smem_addr(ring), S::kBlock);
     auto scores = [&](int i, int st, bool last) {   // S_i = Q_i K^T
       if (elect_one()) {
-        const uint64_t a = dq + i * kStep, b = dk + st * kStep;
+        const uint64_t a = lone ? dq : dq + i * kStep, b = dk + st * kStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t ko = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u) >> 4;
@@ -249,7 +270,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       }
       __syncwarp();
     };
-    auto output = [&](int i, int st, int half, bool first) {   // O_i += P_i V, half of the keys
+    auto output = [&](int i, int st, int half, bool first, bool last) {   // O_i += P_i V, half of the keys
       if (elect_one()) {
         const uint64_t b = dv + st * kStep;
 #pragma unroll
@@ -260,41 +281,51 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
         }
         if (half == 1) {
           umma_commit(&s_o[i]);
-          if (i == nq - 1) umma_commit(&s_empty[st]);
+          if (last) umma_commit(&s_empty[st]);
         }
       }
       __syncwarp();
     };
-    // a ring position: unit u in stage st, phase ph
-    auto full = [&](int st, uint32_t ph) { return mbar_wait(&s_full[st], ph, status); };
-    bool ok = mbar_wait(&s_q, 0, status) && full(0, 0);
-    tc_fence_after();
-    if (ok)
-      for (int i = 0; i < nq; ++i) scores(i, 0, i == nq - 1);
-    int fixes = 0, st = 1;
+    int st = 0, fixes = 0;
     uint32_t ph = 0;
+    auto full = [&]() { return mbar_wait(&s_full[st], ph, status); };   // the ring's next unit
+    auto next = [&]() { if (++st == S::kStages) { st = 0; ph ^= 1; } };
+    bool ok = mbar_wait(&s_q, 0, status) && full();
+    tc_fence_after();
+    if (ok) {
+      scores(0, st, lone);
+      if (!lone) scores(1, st, true);
+      next();
+      if (lone && n > 1 && (ok = full())) {
+        tc_fence_after();
+        scores(1, st, true);
+        next();
+      }
+    }
     for (int j = 0; j < n && ok; ++j) {
       const bool fix = diagonal(it.t0 + j);
-      if (!(ok = full(st, ph))) break;   // V_j
+      if (!(ok = full())) break;   // V_j
       if (fix && lane == 0) mbar_arrive(&s_go);
       const int sv = st;
-      if (++st == S::kStages) { st = 0; ph ^= 1; }
-      for (int i = 0; i < nq && ok; ++i) {
-        ok = mbar_wait(&s_p[i][0], (uint32_t)j & 1u, status);
-        if (ok && fix && i == 0) ok = mbar_wait(&s_fixed, (uint32_t)fixes++ & 1u, status);
+      next();
+      const int i0 = lone ? j & 1 : 0, i1 = lone ? i0 : 1;
+      const uint32_t pp = (uint32_t)(lone ? j >> 1 : j) & 1u;
+      for (int i = i0; i <= i1; ++i) {
+        ok = mbar_wait(&s_p[i][0], pp, status);
+        if (ok && fix && i == i0) ok = mbar_wait(&s_fixed, (uint32_t)fixes++ & 1u, status);
         if (!ok) break;
         tc_fence_after();
-        output(i, sv, 0, j == 0);
-        if (!(ok = mbar_wait(&s_p[i][1], (uint32_t)j & 1u, status))) break;
+        output(i, sv, 0, j < ahead, false);
+        if (!(ok = mbar_wait(&s_p[i][1], pp, status))) break;
         tc_fence_after();
-        output(i, sv, 1, false);
-        if (j + 1 < n) {
-          if (i == 0 && !(ok = full(st, ph))) break;   // K_(j + 1)
+        output(i, sv, 1, false, i == i1);
+        if (j + ahead < n) {
+          if (i == i0 && !(ok = full())) break;   // K_(j + ahead)
           tc_fence_after();
-          scores(i, st, i == nq - 1);
+          scores(i, st, i == i1);
         }
       }
-      if (++st == S::kStages) { st = 0; ph ^= 1; }
+      if (j + ahead < n) next();
     }
     // every MMA issued has completed before the columns are released
     if (elect_one()) umma_commit(&s_done);
@@ -303,11 +334,12 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   } else if (warp >= 10 && n > 0) {
     // ------------------------------------------- value tiles on the diagonal
     int fixes = 0;
-    for (int j = 0; j < n; ++j) {
+    for (int j = max(0, (first_pos + 1) / kRows - it.t0); j < n; ++j) {   // first_pos + 1: the first masked key
       const int t = it.t0 + j;
-      if (!diagonal(t)) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&s_go, (uint32_t)fixes++ & 1u, status))) break;
-      unsigned char* tile = ring + (size_t)((2 * j + 1) % S::kStages) * S::kTile;
+      // V_j's unit: `ahead` keys (all n, if fewer) came first, then one more with every value
+      const int u = j + min(n, j + ahead);
+      unsigned char* tile = ring + (size_t)(u % S::kStages) * S::kTile;
       constexpr int CH = D / 8;
       const int r0 = max(0, first_pos + 1 - t * kRows);    // the first row some query does not see
       const int r1 = min(kRows, it.key_end - t * kRows);   // the first row none sees
@@ -341,16 +373,17 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int i = warp >> 2, r = i * kRows + 32 * (warp & 3) + lane;
+    const int i = warp >> 2, r = (lone ? 0 : i * kRows) + 32 * (warp & 3) + lane;
     const int pos = it.pos0 + ((it.row0 + r) >> tb.g_shift);
     const int warp_pos = __shfl_sync(0xffffffffu, pos, 0);
-    const bool used = i * kRows + 32 * (warp & 3) < it.rows;   // some row of the warp is real
+    const bool used = r - lane < it.rows;   // some row of the warp is real
+    const int turns = lone ? (n - i + 1) >> 1 : n;   // its key tiles: all, or every other one from the i-th
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + S::kS + i * 128, to = tmem + lanes + S::kO + i * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    if (i < nq) {
-      for (int j = 0; j < n && ok; ++j) {
+    {
+      for (int j = 0; j < turns && ok; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(&s_s[i], (uint32_t)j & 1u, status));
         if (!ok) break;
         if (used) {
@@ -362,7 +395,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           tmem_ld32_issue(ts + 96, x[3]);
           tmem_wait_ld();
           tie32(x[0]); tie32(x[1]); tie32(x[2]); tie32(x[3]);
-          const int base = (it.t0 + j) * kRows;
+          const int base = (it.t0 + (lone ? 2 * j + i : j)) * kRows;
           if (base + kRows - 1 > warp_pos) {
             const int lim = pos - base;   // columns above it are masked
 #pragma unroll
@@ -436,10 +469,41 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           mbar_arrive(&s_p[i][1]);
         }
       }
-      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_o[i], (uint32_t)(n - 1) & 1u, status));
+      if (turns > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_o[i], (uint32_t)(turns - 1) & 1u, status));
     }
-    if (used) {
-      tc_fence_after();
+    tc_fence_after();
+    // a lone query tile: group 1 hands its part over in the queries' memory
+    // (every product that read them has completed), 16-byte chunks swizzled
+    // by row
+    float* row1 = reinterpret_cast<float*>(sq) + (32 * (warp & 3) + lane) * D;
+    float c0 = 1.f, c1 = 0.f;
+    if (lone) {
+      if (i == 1 && used && turns > 0) {
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t y[32];
+          tmem_ld32_issue(to + 32 * q, y);
+          tmem_wait_ld();
+          tie32(y);
+          if (r < it.rows)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(row1 + 4 * ((8 * q + e) ^ (lane & 7))) =
+                  make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        }
+      }
+      if (i == 1) s_ml[r] = make_float2(m, l);
+      named_sync(1, 256);
+      if (i == 0) {
+        const float2 ml = s_ml[r];
+        const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+        c0 = ex2(m - mu);
+        c1 = ex2(ml.x - mu);
+        l = c0 * l + c1 * ml.y;
+        m = mn;
+      }
+    }
+    if (used && !(lone && i == 1)) {
       const int row = it.row0 + r;
       const int64_t tok = it.q0 + (row >> tb.g_shift);
       const int head = it.h * G + (row & (G - 1));
@@ -455,6 +519,15 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           tmem_ld32_issue(to + 32 * q, y);
           tmem_wait_ld();
           tie32(y);
+          if (lone && n > 1 && real)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 f = *reinterpret_cast<const float4*>(row1 + 4 * ((8 * q + e) ^ (lane & 7)));
+              const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[4 * e + k] = __float_as_uint(fmaf(c1, v[k], c0 * __uint_as_float(y[4 * e + k])));
+            }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = 0u;
