@@ -34,20 +34,25 @@ __device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT)
   }
   const AttendSeq& s = tb.seq[lo];
   Item it;
-  const int x = item - s.item0, split = x % s.ns, y = x / s.ns;
-  const int blk = s.nblk - 1 - y / tb.hkv, all = s.n << tb.g_shift;
-  it.h = y % tb.hkv;
+  const uint32_t ns = s.ns, x = item - s.item0, y = x / ns, split = x - y * ns;
+  const uint32_t up = y / (uint32_t)tb.hkv;
+  const int blk = s.nblk - 1 - (int)up, all = s.n << tb.g_shift;
+  it.h = (int)(y - up * tb.hkv);
   it.b = s.b; it.T = s.T; it.n = s.n; it.q0 = s.q0;
   it.row0 = blk * tb.rows;
   it.rows = min(tb.rows, all - it.row0);
   it.pos0 = s.T - s.n;
   it.key_end = it.pos0 + ((it.row0 + it.rows - 1) >> tb.g_shift) + 1;
-  const int64_t nt = (it.key_end + KT - 1) / KT;
-  it.t0 = (int)(nt * split / s.ns);
-  it.t1 = (int)(nt * (split + 1) / s.ns);
+  const uint32_t nt = (uint32_t)(it.key_end + KT - 1) / KT;   // at most 2^31 / 32
+  it.t0 = 0;
+  it.t1 = (int)nt;
   it.part = -1;
-  if (s.ns > 1)
+  if (ns > 1) {
+    const uint32_t each = nt / ns, rest = nt - each * ns;   // the first `rest` runs take one more
+    it.t0 = (int)(each * split + min(rest, split));
+    it.t1 = it.t0 + (int)(each + (split < rest));
     it.part = s.part0 + (((int64_t)blk * tb.hkv + it.h) * s.ns + split) * min(tb.rows, all);
+  }
   return it;
 }
 

@@ -8,9 +8,7 @@
 // Roles:
 //   warps 0..3, 4..7  softmax of query tile 0, 1: a thread owns a row
 //                     (a tensor-memory lane), so its maximum, mass and output
-//                     scale need no exchange; a lone query tile (single
-//                     tokens, short prompts) has its key tiles taken in turns
-//                     by both;
+//                     scale need no exchange;
 //   warp 8            the queries (one 3-D tensor copy a tile and 64
 //                     channels), then K_0, V_0, K_1, V_1, ... into a ring of
 //                     stages: a tensor copy per page and 64 channels;
@@ -39,7 +37,7 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a query tile, keys of a key tile
 constexpr int kUThreads = 384;
-constexpr float kRescale = 8.f;     // log2 of the growth that forces a rescale
+constexpr float kRescale = 24.f;     // log2 of the growth that forces a rescale
 constexpr int kPoly = 4;            // every kPoly-th pair of weights without the special-function unit
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kUThreads * 168, "within the launch's registers");
@@ -62,6 +60,22 @@ __device__ __forceinline__ void tensor_load_3d(void* smem, const void* tmap, int
       "r"(smem_addr(bar)) : "memory");
 }
 
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  const uint32_t b = smem_addr(bar);
+  if (try_bar(b, parity)) return true;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kSpinLimit; ++i)
+    if (try_bar(b, parity)) return true;
+  atomicOr(status, WI_DEV_TIMEOUT);
+  return false;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -84,6 +98,35 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
   p = __ffma2_rn(p, f, two(1.f));
   return make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + __float_as_uint(p.x)),
                      __uint_as_float((__float_as_uint(t.y) << 23) + __float_as_uint(p.y)));
+}
+// Lane l of four has chunk c of row l in x[c]; afterwards chunk l of row c: the
+// four lanes' stores of one row are 64 consecutive bytes.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const bool hi = (lane & o) != 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & o) continue;
+      uint4 &a = x[c], &b = x[c | o];
+      const uint4 send = hi ? a : b;
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, send.x, o);
+      got.y = __shfl_xor_sync(0xffffffffu, send.y, o);
+      got.z = __shfl_xor_sync(0xffffffffu, send.z, o);
+      got.w = __shfl_xor_sync(0xffffffffu, send.w, o);
+      if (hi) a = got; else b = got;
+    }
+  }
+}
+// eight bf16 values: some is infinite or NaN
+__device__ __forceinline__ bool nonfinite(const uint4& x) {
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  __nv_bfloat162 a = zero;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), zero, a);
+  return __hisnan(a.x) || __hisnan(a.y);
 }
 // true in one lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -109,8 +152,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   unsigned char* sq = align_smem_1024(sh_raw);
   unsigned char* ring = sq + 2 * S::kTile;
   __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
-  __shared__ __align__(8) uint64_t s_q, s_s[2], s_p[2][2], s_o[2], s_go, s_fixed, s_done;
-  __shared__ float2 s_ml[kRows];
+  __shared__ __align__(8) uint64_t s_q, s_s[2], s_p[2][2], s_o[2], s_go[2], s_fixed[2], s_done;
   __shared__ uint32_t s_tmem, s_bad;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler)
@@ -126,9 +168,9 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       mbar_init(&s_p[i][0], 4);
       mbar_init(&s_p[i][1], 4);
       mbar_init(&s_o[i], 1);
+      mbar_init(&s_go[i], 1);
+      mbar_init(&s_fixed[i], 2);
     }
-    mbar_init(&s_go, 1);
-    mbar_init(&s_fixed, 2);
     mbar_init(&s_done, 1);
     mbar_init_fence();
     s_bad = 0;
@@ -141,20 +183,17 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
 
   const Item it = item_of(tb, blockIdx.x, kRows);
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
-  // Two query tiles take every key tile each; a lone one has its key tiles
-  // taken in turns by the two softmax groups, each with its own (m, l, O).
-  const bool lone = it.rows <= kRows;
-  const int ahead = lone ? 2 : 1;   // key tiles whose scores are under way
+  const int nq = it.rows > kRows ? 2 : 1;
   const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
-  // a key tile on the diagonal: some row of the block does not see all of it
-  auto diagonal = [&](int t) { return t * kRows + kRows - 1 > first_pos; };
+  // the first key tile on the diagonal: with a key (first_pos + 1, say) that
+  // some row of the block does not see
+  const int fix_from = max(0, (first_pos + 1) / kRows - it.t0);
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8 && n > 0) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
-      const int nq = lone ? 1 : 2;
       mbar_arrive_expect(&s_q, (uint32_t)nq * S::kTile);
       for (int i = 0; i < nq; ++i)
         for (int c = 0; c < S::kBlocks; ++c)
@@ -170,45 +209,36 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       const int r_shift = min(kp.page_shift, 7), per = kRows >> r_shift;
       const int bx = lane & (per - 1), c = lane / per;
       const int none = (int)((kp.n_pages * tb.hkv) << kp.page_shift);
-      auto page_at = [&](int j) {   // of this lane's box in key tile j (looked up tiles ahead of its use)
-        const int key = (it.t0 + j) * kRows + (bx << r_shift);
-        return j < n && key < it.key_end ? __ldg(bt + (key >> kp.page_shift)) : INT32_MAX;
+      auto page_at = [&](int t) {
+        const int key = t * kRows + (bx << r_shift);
+        return key < it.key_end && t < it.t1 ? __ldg(bt + (key >> kp.page_shift)) : -1;
       };
-      auto row_at = [&](int j, int page) {
-        const int key = (it.t0 + j) * kRows + (bx << r_shift);
-        if (page >= 0 && page < kp.n_pages)
-          return ((page * tb.hkv + it.h) << kp.page_shift) + (key & page_mask);
-        if (j < n && key < it.key_end) flag_error(status, WI_DEV_BAD_PAGE);
-        return none;
-      };
-      // unit u: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead) in turns; a
-      // tile's row is kept from its keys to its values
-      int issued = 0, st = 0, page = page_at(2);
-      int y0 = row_at(0, page_at(0)), y1 = row_at(1, page_at(1));
-      uint32_t ph = 1;
-      auto load = [&](const CUtensorMap* map, int row) {
-        if (issued >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[st], ph, status));
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect(&s_full[st], S::kTile);
-        __syncwarp();
-        if (c < S::kBlocks)
-          tensor_load_2d(ring + (size_t)st * S::kTile + c * S::kBlock + (bx << r_shift) * 128, map, 64 * c, row, &s_full[st]);
-        ++issued;
-        if (++st == S::kStages) { st = 0; ph ^= 1; }
-      };
-      load(&map_k, y0);
-      if (lone && n > 1) load(&map_k, y1);
+      int page = page_at(it.t0), issued = 0;
       for (int j = 0; j < n && ok; ++j) {
-        const int y2 = row_at(j + 2, page);
-        page = page_at(j + 3);
-        load(&map_v, y0);
-        if (ok && j + ahead < n) load(&map_k, lone ? y2 : y1);
-        y0 = y1;
-        y1 = y2;
+        const int t = it.t0 + j, key = t * kRows + (bx << r_shift);
+        int y = none;
+        if (key < it.key_end) {
+          if (page >= 0 && page < kp.n_pages)
+            y = ((page * tb.hkv + it.h) << kp.page_shift) + (key & page_mask);
+          else
+            flag_error(status, WI_DEV_BAD_PAGE);
+        }
+        page = page_at(t + 1);
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const int u = 2 * j + kv, st = u % S::kStages;
+          if (u >= S::kStages) ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect(&s_full[st], S::kTile);
+          __syncwarp();
+          if (c < S::kBlocks)
+            tensor_load_2d(ring + (size_t)st * S::kTile + c * S::kBlock + (bx << r_shift) * 128,
+                           kv ? &map_v : &map_k, 64 * c, y, &s_full[st]);
+          issued = u + 1;
+        }
       }
       if (!ok)   // a wait gave up: no copy is left in flight when the CTA ends
         for (int u = max(0, issued - S::kStages); u < issued; ++u)
-          mbar_wait(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
+          wait_bar(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
     } else {
       // pages of fewer than 8 rows: 16-byte copies into the swizzled layout,
       // two units behind the one being issued
@@ -220,15 +250,10 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       };
       int u = 0;
       for (; u < 2 * n && ok; ++u) {
-        // the same order: past the first `ahead`, values at every other unit
-        // until the keys have run out
-        const int x = u - min(ahead, n), keys_left = 2 * (n - min(ahead, n));
-        const bool val = x >= 0 && ((x & 1) == 0 || x >= keys_left);
-        const int j = x < 0 ? u : x >= keys_left ? x - keys_left / 2 : val ? x / 2 : x / 2 + ahead;
-        const int t = it.t0 + j, st = u % S::kStages;
-        if (u >= S::kStages) ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
+        const int t = it.t0 + u / 2, st = u % S::kStages;
+        if (u >= S::kStages) ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
         if (!ok) break;
-        const Pool& p = val ? vp : kp;
+        const Pool& p = u & 1 ? vp : kp;
         unsigned char* dst = ring + (size_t)st * S::kTile;
 #pragma unroll 4
         for (int i = lane; i < kRows * CH; i += 32) {
@@ -259,7 +284,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
     const uint64_t dv = umma_desc_sw128_mn(smem_addr(ring), S::kBlock);
     auto scores = [&](int i, int st, bool last) {   // S_i = Q_i K^T
       if (elect_one()) {
-        const uint64_t a = lone ? dq : dq + i * kStep, b = dk + st * kStep;
+        const uint64_t a = dq + i * kStep, b = dk + st * kStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t ko = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u) >> 4;
@@ -270,7 +295,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
       }
       __syncwarp();
     };
-    auto output = [&](int i, int st, int half, bool first, bool last) {   // O_i += P_i V, half of the keys
+    auto output = [&](int i, int st, int half, bool first) {   // O_i += P_i V, half of the keys
       if (elect_one()) {
         const uint64_t b = dv + st * kStep;
 #pragma unroll
@@ -281,110 +306,114 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
         }
         if (half == 1) {
           umma_commit(&s_o[i]);
-          if (last) umma_commit(&s_empty[st]);
+          if (i == nq - 1) umma_commit(&s_empty[st]);
         }
       }
       __syncwarp();
     };
-    int st = 0, fixes = 0;
-    uint32_t ph = 0;
-    auto full = [&]() { return mbar_wait(&s_full[st], ph, status); };   // the ring's next unit
-    auto next = [&]() { if (++st == S::kStages) { st = 0; ph ^= 1; } };
-    bool ok = mbar_wait(&s_q, 0, status) && full();
+    // a ring position: unit u in stage st, phase ph
+    auto full = [&](int st, uint32_t ph) { return wait_bar(&s_full[st], ph, status); };
+    bool ok = wait_bar(&s_q, 0, status) && full(0, 0);
     tc_fence_after();
-    if (ok) {
-      scores(0, st, lone);
-      if (!lone) scores(1, st, true);
-      next();
-      if (lone && n > 1 && (ok = full())) {
-        tc_fence_after();
-        scores(1, st, true);
-        next();
-      }
-    }
+    if (ok)
+      for (int i = 0; i < nq; ++i) scores(i, 0, i == nq - 1);
+    if (fix_from == 0 && lane == 0) mbar_arrive(&s_go[0]);
+    int st = 1;
+    uint32_t ph = 0;
     for (int j = 0; j < n && ok; ++j) {
-      const bool fix = diagonal(it.t0 + j);
-      if (!(ok = full())) break;   // V_j
-      if (fix && lane == 0) mbar_arrive(&s_go);
+      // the diagonal's values are looked at a tile ahead of their product
+      if (j + 1 >= fix_from && j + 1 < n && lane == 0) mbar_arrive(&s_go[(j + 1) & 1]);
+      const bool fix = j >= fix_from;
+      if (!(ok = full(st, ph))) break;   // V_j
       const int sv = st;
-      next();
-      const int i0 = lone ? j & 1 : 0, i1 = lone ? i0 : 1;
-      const uint32_t pp = (uint32_t)(lone ? j >> 1 : j) & 1u;
-      for (int i = i0; i <= i1; ++i) {
-        ok = mbar_wait(&s_p[i][0], pp, status);
-        if (ok && fix && i == i0) ok = mbar_wait(&s_fixed, (uint32_t)fixes++ & 1u, status);
+      if (++st == S::kStages) { st = 0; ph ^= 1; }
+      for (int i = 0; i < nq && ok; ++i) {
+        ok = wait_bar(&s_p[i][0], (uint32_t)j & 1u, status);
+        if (ok && fix && i == 0) ok = wait_bar(&s_fixed[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
         if (!ok) break;
         tc_fence_after();
-        output(i, sv, 0, j < ahead, false);
-        if (!(ok = mbar_wait(&s_p[i][1], pp, status))) break;
+        output(i, sv, 0, j == 0);
+        if (!(ok = wait_bar(&s_p[i][1], (uint32_t)j & 1u, status))) break;
         tc_fence_after();
-        output(i, sv, 1, false, i == i1);
-        if (j + ahead < n) {
-          if (i == i0 && !(ok = full())) break;   // K_(j + ahead)
+        output(i, sv, 1, false);
+        if (j + 1 < n) {
+          if (i == 0 && !(ok = full(st, ph))) break;   // K_(j + 1)
           tc_fence_after();
-          scores(i, st, i == i1);
+          scores(i, st, i == nq - 1);
         }
       }
-      if (j + ahead < n) next();
+      if (++st == S::kStages) { st = 0; ph ^= 1; }
     }
     // every MMA issued has completed before the columns are released
     if (elect_one()) umma_commit(&s_done);
     __syncwarp();
-    mbar_wait(&s_done, 0, status);
+    wait_bar(&s_done, 0, status);
   } else if (warp >= 10 && n > 0) {
     // ------------------------------------------- value tiles on the diagonal
-    int fixes = 0;
-    for (int j = max(0, (first_pos + 1) / kRows - it.t0); j < n; ++j) {   // first_pos + 1: the first masked key
-      const int t = it.t0 + j;
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_go, (uint32_t)fixes++ & 1u, status))) break;
-      // V_j's unit: `ahead` keys (all n, if fewer) came first, then one more with every value
-      const int u = j + min(n, j + ahead);
+    for (int j = fix_from; j < n; ++j) {
+      // (the ring's phase of V_j is known only from a permission in the MMA
+      // warp's order; two of them alternate, as the next may come before this
+      // one is seen)
+      const int u = 2 * j + 1, base = (it.t0 + j) * kRows;
+      bool ok = wait_bar(&s_go[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
+      ok = ok && wait_bar(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
       unsigned char* tile = ring + (size_t)(u % S::kStages) * S::kTile;
       constexpr int CH = D / 8;
-      const int r0 = max(0, first_pos + 1 - t * kRows);    // the first row some query does not see
-      const int r1 = min(kRows, it.key_end - t * kRows);   // the first row none sees
+      auto chunk_at = [&](int c) {
+        return reinterpret_cast<uint4*>(tile + ((c % CH) >> 3) * S::kBlock + swz128(c / CH, c & 7));
+      };
+      const int r0 = max(0, first_pos + 1 - base);   // the first row some query does not see
+      const int r1 = min(kRows, it.key_end - base);     // the first row none sees
+      const int at0 = 32 * (warp - 10) + lane;
+#pragma unroll 4
+      for (int c = r1 * CH + at0; c < kRows * CH; c += 64) *chunk_at(c) = make_uint4(0u, 0u, 0u, 0u);
+      // four chunks in flight; a product with 0 tells whether all eight
+      // values of a chunk are finite (0 or NaN)
       bool bad = false;
-      for (int i = r0 * CH + (tid - 320); i < kRows * CH; i += 64) {
-        const int r = i / CH, ch = i % CH;
-        uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * S::kBlock + swz128(r, ch & 7));
-        if (r >= r1) {
-          *at = make_uint4(0u, 0u, 0u, 0u);
-          continue;
-        }
-        uint4 x = *at;
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        bool found = false;
+#pragma unroll 1
+      for (int c0 = r0 * CH + at0; c0 < r1 * CH; c0 += 256) {
+        uint4 x[4];
 #pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = *chunk_at(min(c0 + 64 * e, r1 * CH - 1));
+        uint32_t odd = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= nonfinite(x[e]) ? 1u << e : 0u;
+        if (odd == 0) continue;
+#pragma unroll 1
         for (int e = 0; e < 4; ++e) {
-          if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; found = true; }
-          if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0x0000ffffu; found = true; }
-        }
-        if (found) {
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
+          if (!((odd >> e) & 1u) || c0 + 64 * e >= r1 * CH) continue;
+          uint32_t* w = reinterpret_cast<uint32_t*>(chunk_at(c0 + 64 * e));
           bad = true;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v = w[q];
+            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+            w[q] = v;
+          }
         }
       }
       if (bad) atomicOr(&s_bad, 1u);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_fixed);
+      if (lane == 0) mbar_arrive(&s_fixed[j & 1]);
     }
   }
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int i = warp >> 2, r = (lone ? 0 : i * kRows) + 32 * (warp & 3) + lane;
+    const int i = warp >> 2, r = i * kRows + 32 * (warp & 3) + lane;
     const int pos = it.pos0 + ((it.row0 + r) >> tb.g_shift);
     const int warp_pos = __shfl_sync(0xffffffffu, pos, 0);
-    const bool used = r - lane < it.rows;   // some row of the warp is real
-    const int turns = lone ? (n - i + 1) >> 1 : n;   // its key tiles: all, or every other one from the i-th
+    const bool used = i * kRows + 32 * (warp & 3) < it.rows;   // some row of the warp is real
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + S::kS + i * 128, to = tmem + lanes + S::kO + i * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    {
-      for (int j = 0; j < turns && ok; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_s[i], (uint32_t)j & 1u, status));
+    if (i < nq) {
+      for (int j = 0; j < n && ok; ++j) {
+        ok = __all_sync(0xffffffffu, wait_bar(&s_s[i], (uint32_t)j & 1u, status));
         if (!ok) break;
         if (used) {
           tc_fence_after();
@@ -395,7 +424,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           tmem_ld32_issue(ts + 96, x[3]);
           tmem_wait_ld();
           tie32(x[0]); tie32(x[1]); tie32(x[2]); tie32(x[3]);
-          const int base = (it.t0 + (lone ? 2 * j + i : j)) * kRows;
+          const int base = (it.t0 + j) * kRows;
           if (base + kRows - 1 > warp_pos) {
             const int lim = pos - base;   // columns above it are masked
 #pragma unroll
@@ -424,18 +453,10 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
             l *= c;
             m = mn;
             if (j > 0) {   // O holds the keys before
-              ok = __all_sync(0xffffffffu, mbar_wait(&s_o[i], (uint32_t)(j - 1) & 1u, status));
+              ok = __all_sync(0xffffffffu, wait_bar(&s_o[i], (uint32_t)(j - 1) & 1u, status));
               tc_fence_after();
-#pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t y[32];
-                tmem_ld32_issue(to + 32 * q, y);
-                tmem_wait_ld();
-                tie32(y);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * c);
-                tmem_st32(to + 32 * q, y);
-              }
+#pragma unroll 1
+              for (int q = 0; q < D; q += 8) tmem_scale8(to + q, c);
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
@@ -469,98 +490,76 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           mbar_arrive(&s_p[i][1]);
         }
       }
-      if (turns > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_o[i], (uint32_t)(turns - 1) & 1u, status));
+      if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&s_o[i], (uint32_t)(n - 1) & 1u, status));
     }
-    tc_fence_after();
-    // a lone query tile: group 1 hands its part over in the queries' memory
-    // (every product that read them has completed), 16-byte chunks swizzled
-    // by row
-    float* row1 = reinterpret_cast<float*>(sq) + (32 * (warp & 3) + lane) * D;
-    float c0 = 1.f, c1 = 0.f;
-    if (lone) {
-      if (i == 1 && used && turns > 0) {
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t y[32];
-          tmem_ld32_issue(to + 32 * q, y);
-          tmem_wait_ld();
-          tie32(y);
-          if (r < it.rows)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(row1 + 4 * ((8 * q + e) ^ (lane & 7))) =
-                  make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-        }
-      }
-      if (i == 1) s_ml[r] = make_float2(m, l);
-      named_sync(1, 256);
-      if (i == 0) {
-        const float2 ml = s_ml[r];
-        const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-        c0 = ex2(m - mu);
-        c1 = ex2(ml.x - mu);
-        l = c0 * l + c1 * ml.y;
-        m = mn;
-      }
-    }
-    if (used && !(lone && i == 1)) {
+    if (used) {
+      tc_fence_after();
       const int row = it.row0 + r;
       const int64_t tok = it.q0 + (row >> tb.g_shift);
       const int head = it.h * G + (row & (G - 1));
       const bool real = r < it.rows;
       const float inv = 1.f / l;
+      auto out_row = [&](int rr) {   // of row rr of the block
+        const int x = it.row0 + rr;
+        return reinterpret_cast<T*>(ao.out) + (it.q0 + (x >> tb.g_shift)) * ao.stride +
+               (int64_t)(it.h * G + (x & (G - 1))) * D;
+      };
       if (real && it.part >= 0) ao.ml[it.part + r] = make_float2(m, l);
       else if (real && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m + log2f(l));
-      const bool give_back = *(volatile uint32_t*)&s_bad != 0;
+      // 64 bytes of a row at a time (16 columns of a part, 32 of the output);
+      // four lanes store a row's together: row 4 (lane / 4) + c of the warp
+      const bool part = it.part >= 0;
+      const int r4 = r - lane + (lane & ~3);
+      uint4 x[4];
+#pragma unroll 1
+      for (int col = 0; col < D; col += 16) {
+        uint32_t y[16];
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t y[32];
-        if (n > 0) {
-          tmem_ld32_issue(to + 32 * q, y);
-          tmem_wait_ld();
-          tie32(y);
-          if (lone && n > 1 && real)
+        for (int e = 0; e < 16; ++e) y[e] = 0u;
+        if (n > 0) tmem_ld16(to + col, y);
+        if (part) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 f = *reinterpret_cast<const float4*>(row1 + 4 * ((8 * q + e) ^ (lane & 7)));
-              const float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[4 * e + k] = __float_as_uint(fmaf(c1, v[k], c0 * __uint_as_float(y[4 * e + k])));
-            }
+          for (int c = 0; c < 4; ++c) x[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
         } else {
+          x[0] = x[2];
+          x[1] = x[3];
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0u;
+          for (int e = 0; e < 8; ++e)
+            w[e] = pack_bf16(__uint_as_float(y[2 * e]) * inv, __uint_as_float(y[2 * e + 1]) * inv);
+          x[2] = make_uint4(w[0], w[1], w[2], w[3]);
+          x[3] = make_uint4(w[4], w[5], w[6], w[7]);
+          if (!(col & 16)) continue;
         }
-        if (give_back && real) {
-          // values that are not finite, to the rows that see them (a positive
-          // weight of them is they themselves)
-          const int p1 = min(pos + 1, it.t1 * kRows);
-          for (int p = max(first_pos + 1, it.t0 * kRows); p < p1; ++p) {
-            const int64_t at = pool_row(vp, tb.hkv, D, it.b, it.h, p, status);
-            if (at < 0) continue;
-            const T* v = reinterpret_cast<const T*>(vp.base) + at + 32 * q;
+        uint4 t[4] = {x[0], x[1], x[2], x[3]};
+        transpose4(t, lane);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float f = __bfloat162float(v[e]);
-              if (!isfinite(f)) y[e] = __float_as_uint(__uint_as_float(y[e]) + f);
+        for (int c = 0; c < 4; ++c) {
+          if (r4 + c >= it.rows) break;
+          unsigned char* o = part ? reinterpret_cast<unsigned char*>(ao.o + (it.part + r4 + c) * D + col)
+                                  : reinterpret_cast<unsigned char*>(out_row(r4 + c) + (col & ~16));
+          *reinterpret_cast<uint4*>(o + 16 * (lane & 3)) = t[c];
+        }
+      }
+      if (*(volatile uint32_t*)&s_bad != 0) {
+        // values that are not finite, added to the rows that see them (a
+        // positive weight of them is they themselves)
+        __syncwarp();
+        const int p1 = real ? min(pos + 1, it.t1 * kRows) : 0;
+#pragma unroll 1
+        for (int p = max(first_pos + 1, it.t0 * kRows); p < p1; ++p) {
+          const int64_t at = pool_row(vp, tb.hkv, D, it.b, it.h, p, status);
+#pragma unroll 1
+          for (int c = 0; at >= 0 && c < D; ++c) {
+            const float f = __bfloat162float(reinterpret_cast<const T*>(vp.base)[at + c]);
+            if (isfinite(f)) continue;
+            if (part) {
+              ao.o[(it.part + r) * D + c] += f;
+            } else {
+              T* o = out_row(r) + c;
+              *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
             }
           }
-        }
-        if (real && it.part >= 0) {
-          float* o = ao.o + (it.part + r) * D + 32 * q;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(o + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-        } else if (real) {
-          T* o = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D + 32 * q;
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16(__uint_as_float(y[2 * e]) * inv, __uint_as_float(y[2 * e + 1]) * inv);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(o + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         }
       }
       tc_fence_before();
