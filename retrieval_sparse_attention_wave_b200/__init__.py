@@ -257,6 +257,12 @@ class KVCache:
         return self.k_pool.shape[3]
 
     def c_struct(self) -> WiKVCache:
+        # kept while the buffers it points at are the same (a step per layer
+        # marshals the same cache)
+        sig = (self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.block_table.data_ptr(),
+               self.k_pool.shape, self.k_pool.dtype, self.block_table.shape, id(self._seq))
+        if getattr(self, "_cs_sig", None) == sig:
+            return self._cs
         s = WiKVCache()
         s.dtype = _dtype_code(self.k_pool.dtype)
         s.batch = len(self.seq_lens)
@@ -269,6 +275,7 @@ class KVCache:
         s.block_table = self.block_table.data_ptr()
         s.max_pages = self.block_table.shape[1]
         s.seq_lens = C.cast(self._seq, C.POINTER(C.c_int32))
+        self._cs, self._cs_sig = s, sig
         return s
 
 
@@ -573,49 +580,47 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_gpu(name: str, t: torch.Tensor, dtype, like: Optional[torch.Tensor] = None, shape=None):
+def _on_gpu(name: str, t: torch.Tensor, dtype, dev: int, shape=None):
     """Argument checks of the serving calls (the library sees only pointers)."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor is expected, got "
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor on cuda:{dev} is expected, got "
                          f"{t.dtype} on {t.device}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, the call's other tensors on {like.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is expected, got one on {t.device}")
+    return dev
 
 
 def _token_rows(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
     """Checks [tokens][heads][d] rows (a view of wider rows is fine: only the
     token stride may differ from contiguous); returns the token stride."""
-    _need(t.dim() == 3 and t.dtype == like.dtype and t.device == like.device,
-          f"{name}: a [tokens][heads][head_dim] {like.dtype} tensor on {like.device} is expected")
+    if t.dim() != 3 or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name}: a [tokens][heads][head_dim] {like.dtype} tensor on {like.device} is expected")
     n, heads, d = t.shape
-    _need((d == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d),
-          f"{name}: the heads of a token must be contiguous")
-    _need(n <= 1 or t.stride(0) >= heads * d, f"{name}: token rows must not overlap")
-    return t.stride(0) if n > 1 else heads * d
+    row, head, step = t.stride()
+    if (d != 1 and step != 1) or (heads != 1 and head != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if n <= 1:
+        return heads * d
+    if row < heads * d:
+        raise ValueError(f"{name}: token rows must not overlap")
+    return row
 
 
-class _Here:
-    """The call's stream on the tensors' device, and that device current for
-    the launch.  Tensors the call allocates are allocated on that stream."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        _need(self.stream.device == t.device,
-              f"the stream is on {self.stream.device}, the tensors on {t.device}")
-        self.guard = None
-        if stream is not None or t.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return C.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _elsewhere(dev: int, stream):
+    """The stream to make current for a call whose tensors are on `dev`, None
+    when the current stream is the one to use (the common case)."""
+    if dev < 0 or (stream is None and dev == torch.cuda.current_device()):
+        return None   # (not on a GPU: refused by the checks that follow)
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    _need(stream.device.index == dev, f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return None if stream == torch.cuda.current_stream() else stream
 
 
 @dataclass
@@ -673,34 +678,38 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
     slots and positions behind the last one are -1.  A step that does not fit
     plans nothing and sets WI_DEV_NO_PAGES in the workspace's status."""
     bt = table.block_table
+    dev = _device_of("block_table", bt)
+    s = _elsewhere(dev, stream)
+    if s is not None:
+        with torch.cuda.stream(s):
+            return plan_pages(table, new_lens, capacity, out, update, ws)
     _need(bt.dim() == 2, "block_table: [batch][max_pages] is expected")
-    B = bt.shape[0]
-    _on_gpu("block_table", bt, torch.int32)
-    _on_gpu("seq_lens", table.seq_lens, torch.int32, bt, (B,))
-    _on_gpu("new_lens", new_lens, torch.int32, bt, (B,))
-    _on_gpu("free_pages", table.free_pages, torch.int32, bt, (table.free_pages.numel(),))
-    _on_gpu("n_free", table.n_free, torch.int32, bt, (1,))
-    with _Here(bt, stream) as s:
-        if out is None:
-            out = PagePlan.empty(table, capacity, update)
-        else:
-            _need(not update or (out.seq_lens is table.seq_lens and out.n_free is table.n_free),
-                  "update: `out` must hold the table's own seq_lens and n_free")
-            _on_gpu("out.slot_map", out.slot_map, torch.int32, bt, (capacity,))
-            _on_gpu("out.positions", out.positions, torch.int32, bt, (capacity,))
-            _on_gpu("out.starts", out.starts, torch.int32, bt, (B + 1,))
-            _on_gpu("out.seq_lens", out.seq_lens, torch.int32, bt, (B,))
-            _on_gpu("out.n_free", out.n_free, torch.int32, bt, (1,))
-        if ws is None:
-            ws = serve_workspace(bt.device)
-        _on_gpu("ws", ws, torch.uint8, bt)
-        p = WiPagePlan(B, table.page_size, table.n_pages, table.seq_lens.data_ptr(),
-                       new_lens.data_ptr(), bt.data_ptr(), bt.shape[1],
-                       table.free_pages.data_ptr(), table.free_pages.numel(),
-                       table.n_free.data_ptr(), out.seq_lens.data_ptr(), out.n_free.data_ptr(),
-                       out.starts.data_ptr(), capacity, out.slot_map.data_ptr(),
-                       out.positions.data_ptr())
-        _check(_lib.wi_plan_pages(C.byref(p), _ptr(ws), ws.numel(), s), "wi_plan_pages")
+    i32, (B, max_pages) = torch.int32, bt.shape
+    _on_gpu("block_table", bt, i32, dev)
+    _on_gpu("seq_lens", table.seq_lens, i32, dev, (B,))
+    _on_gpu("new_lens", new_lens, i32, dev, (B,))
+    _on_gpu("free_pages", table.free_pages, i32, dev)
+    _on_gpu("n_free", table.n_free, i32, dev, (1,))
+    if out is None:
+        out = PagePlan.empty(table, capacity, update)
+    else:
+        _need(not update or (out.seq_lens is table.seq_lens and out.n_free is table.n_free),
+              "update: `out` must hold the table's own seq_lens and n_free")
+        _on_gpu("out.slot_map", out.slot_map, i32, dev, (capacity,))
+        _on_gpu("out.positions", out.positions, i32, dev, (capacity,))
+        _on_gpu("out.starts", out.starts, i32, dev, (B + 1,))
+        _on_gpu("out.seq_lens", out.seq_lens, i32, dev, (B,))
+        _on_gpu("out.n_free", out.n_free, i32, dev, (1,))
+    if ws is None:
+        ws = serve_workspace(bt.device)
+    _on_gpu("ws", ws, torch.uint8, dev)
+    p = WiPagePlan(B, table.page_size, table.n_pages, table.seq_lens.data_ptr(),
+                   new_lens.data_ptr(), bt.data_ptr(), max_pages, table.free_pages.data_ptr(),
+                   table.free_pages.numel(), table.n_free.data_ptr(), out.seq_lens.data_ptr(),
+                   out.n_free.data_ptr(), out.starts.data_ptr(), capacity,
+                   out.slot_map.data_ptr(), out.positions.data_ptr())
+    _check(_lib.wi_plan_pages(C.byref(p), ws.data_ptr(), ws.numel(),
+                              torch.cuda.current_stream().cuda_stream), "wi_plan_pages")
     return out
 
 
@@ -709,22 +718,29 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
     """Write k, v [tokens][n_kv_heads][head_dim] into the pools' rows at
     slot_map [tokens] (wi_append_kv).  Negative slots are skipped; k and v may
     be views of a fused projection's rows."""
+    dev = k_pool.get_device()
+    s = _elsewhere(dev, stream)
+    if s is not None:
+        with torch.cuda.stream(s):
+            return append_kv(k, v, slot_map, k_pool, v_pool, ws)
     _need(k_pool.dim() == 4 and k_pool.shape == v_pool.shape,
           "k_pool, v_pool: equal [n_pages][n_kv_heads][page_size][head_dim] shapes are expected")
-    _on_gpu("k_pool", k_pool, k_pool.dtype)
-    _on_gpu("v_pool", v_pool, k_pool.dtype, k_pool)
+    _device_of("k_pool", k_pool)
+    _on_gpu("k_pool", k_pool, k_pool.dtype, dev)
+    _on_gpu("v_pool", v_pool, k_pool.dtype, dev)
     n_pages, H, P, d = k_pool.shape
     ks, vs = _token_rows("k", k, k_pool), _token_rows("v", v, k_pool)
     n = k.shape[0]
-    _need(tuple(k.shape) == tuple(v.shape) == (n, H, d), f"k, v: [tokens][{H}][{d}] is expected")
-    _on_gpu("slot_map", slot_map, torch.int32, k_pool, (n,))
-    with _Here(k_pool, stream) as s:
-        if ws is None:
-            ws = serve_workspace(k_pool.device)
-        _on_gpu("ws", ws, torch.uint8, k_pool)
-        a = WiKVAppend(_dtype_code(k_pool.dtype), n, H, d, P, n_pages, k.data_ptr(), v.data_ptr(),
-                       ks, vs, slot_map.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
-        _check(_lib.wi_append_kv(C.byref(a), _ptr(ws), ws.numel(), s), "wi_append_kv")
+    if not (k.shape == v.shape == (n, H, d)):
+        raise ValueError(f"k, v: [tokens][{H}][{d}] is expected")
+    _on_gpu("slot_map", slot_map, torch.int32, dev, (n,))
+    if ws is None:
+        ws = serve_workspace(k_pool.device)
+    _on_gpu("ws", ws, torch.uint8, dev)
+    a = WiKVAppend(_dtype_code(k_pool.dtype), n, H, d, P, n_pages, k.data_ptr(), v.data_ptr(),
+                   ks, vs, slot_map.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
+    _check(_lib.wi_append_kv(C.byref(a), ws.data_ptr(), ws.numel(),
+                             torch.cuda.current_stream().cuda_stream), "wi_append_kv")
 
 
 @dataclass
@@ -735,6 +751,8 @@ class AttendParams:
 
     def __post_init__(self):
         self._q_lens = None if self.q_lens is None else _i32_array(self.q_lens)
+        self._q_ptr = (None if self.q_lens is None
+                       else C.cast(self._q_lens, C.POINTER(C.c_int32)))
 
     def n_queries(self, kv: KVCache) -> int:
         _need(self._q_lens is None or len(self._q_lens) == len(kv.seq_lens),
@@ -742,8 +760,7 @@ class AttendParams:
         return sum(kv.seq_lens if self._q_lens is None else self._q_lens)
 
     def c_struct(self, q_stride: int = 0, out_stride: int = 0) -> WiAttendParams:
-        q_lens = None if self._q_lens is None else C.cast(self._q_lens, C.POINTER(C.c_int32))
-        return WiAttendParams(self.n_q_heads, q_lens, q_stride, out_stride)
+        return WiAttendParams(self.n_q_heads, self._q_ptr, q_stride, out_stride)
 
 
 def attend_workspace_bytes(kv: KVCache, params: AttendParams) -> int:
@@ -767,30 +784,36 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     fp32 [sum q_lens][n_q_heads].  q may have rows behind the last sequence
     (a padded batch): out and lse keep theirs."""
     kp = kv.k_pool
+    dev = kp.get_device()
+    s = _elsewhere(dev, stream)
+    if s is not None:
+        with torch.cuda.stream(s):
+            return attend(q, kv, params, out, lse, ws)
     qs = _token_rows("q", q, kp)
     n, Hq, d = q.shape
-    _need(Hq == params.n_q_heads and d == kv.head_dim,
-          f"q: [tokens][{params.n_q_heads}][{kv.head_dim}] is expected")
+    if Hq != params.n_q_heads or d != kv.head_dim:
+        raise ValueError(f"q: [tokens][{params.n_q_heads}][{kv.head_dim}] is expected")
     _need(n >= params.n_queries(kv), "q: fewer rows than sum(q_lens)")
     _need(kv.v_pool.shape == kp.shape and kv.block_table.dim() == 2
           and kv.block_table.shape[0] == len(kv.seq_lens), "kv: pools and table do not match")
-    _on_gpu("k_pool", kp, kp.dtype)
-    _on_gpu("v_pool", kv.v_pool, kp.dtype, kp)
-    _on_gpu("block_table", kv.block_table, torch.int32, kp)
-    with _Here(kp, stream) as s:
-        if out is None:
-            out = torch.empty(n, Hq, d, dtype=q.dtype, device=q.device)
-        os_ = _token_rows("out", out, kp)
-        _need(out.shape == q.shape, "out: the shape of q is expected")
-        if lse is None:
-            lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
-        _on_gpu("lse", lse, torch.float32, kp, (n, Hq))
-        if ws is None:
-            ws = attend_workspace(kv, params)
-        _on_gpu("ws", ws, torch.uint8, kp)
-        c, p = kv.c_struct(), params.c_struct(qs, os_)
-        _check(_lib.wi_attend(_ptr(q), C.byref(c), C.byref(p), _ptr(out), _ptr(lse), _ptr(ws),
-                              ws.numel(), s), "wi_attend")
+    _device_of("k_pool", kp)
+    _on_gpu("k_pool", kp, kp.dtype, dev)
+    _on_gpu("v_pool", kv.v_pool, kp.dtype, dev)
+    _on_gpu("block_table", kv.block_table, torch.int32, dev)
+    if out is None:
+        out = torch.empty(n, Hq, d, dtype=q.dtype, device=q.device)
+    os_ = _token_rows("out", out, kp)
+    _need(out.shape == q.shape, "out: the shape of q is expected")
+    if lse is None:
+        lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
+    _on_gpu("lse", lse, torch.float32, dev, (n, Hq))
+    if ws is None:
+        ws = attend_workspace(kv, params)
+    _on_gpu("ws", ws, torch.uint8, dev)
+    c, p = kv.c_struct(), params.c_struct(qs, os_)
+    _check(_lib.wi_attend(q.data_ptr(), C.byref(c), C.byref(p), out.data_ptr(), lse.data_ptr(),
+                          ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream),
+           "wi_attend")
     return out, lse
 
 

@@ -212,47 +212,54 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
 }
 
 // ------------------------------------------------------------------ merge
-// One warp per query row of the split sequences: the parts' (m, l) give the
-// weights 2^(m_s - m), then the parts' outputs are added in order.
-constexpr int kMergeThreads = 128;
+// The parts' (m, l) of a query row of a split sequence give the weights
+// 2^(m_s - m); the parts' outputs are added in order.  A warp per row, or,
+// where the rows are few (single tokens), a CTA per row whose four warps take
+// every fourth part and add up in a fixed order.
+constexpr int kMergeWarps = 4;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads)
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(32 * kMergeWarps)
 attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const AttendOut ao) {
   constexpr int E = D / 32;   // columns per lane
-  const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x * (kMergeThreads / 32) + ((int)threadIdx.x >> 5);
+  constexpr int kStep = kWide ? kMergeWarps : 1;
+  __shared__ float s_o[kWide ? kMergeWarps : 1][D], s_l[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  const int x = kWide ? (int)blockIdx.x : (int)blockIdx.x * kMergeWarps + warp;
   int lo = 0, hi = tb.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (tb.seq[mid].mrow0 <= x) lo = mid; else hi = mid - 1;
   }
   const AttendSeq& s = tb.seq[lo];
-  const int all = s.n << tb.g_shift, Rb = min(tb.rows, all);
-  const int h = (x - s.mrow0) / all, row = (x - s.mrow0) % all;
-  const int blk = row / tb.rows, rr = row % tb.rows;
+  const uint32_t all = (uint32_t)s.n << tb.g_shift, Rb = min((uint32_t)tb.rows, all);
+  const uint32_t in = (uint32_t)(x - s.mrow0), h = in / all, row = in - h * all;
+  const uint32_t blk = row / (uint32_t)tb.rows, rr = row - blk * tb.rows;
   const int64_t part = s.part0 + ((int64_t)blk * tb.hkv + h) * s.ns * Rb + rr;
+  const int ns = s.ns;
   pdl_wait();   // the parts are there
   if (x >= n_rows) return;
   float m = -INFINITY;
-  for (int i = lane; i < s.ns; i += 32) m = fmaxf(m, __ldcg(&ao.ml[part + (int64_t)i * Rb]).x);
+  for (int i = lane; i < ns; i += 32) m = fmaxf(m, __ldcg(&ao.ml[part + (int64_t)i * Rb]).x);
   m = warp_max(m);
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int i0 = 0; i0 < s.ns; i0 += 32) {
+  // parts first, first + kStep, ..., 32 of them at a time
+  const int first = kWide ? warp : 0;
+  for (int i0 = first; i0 < ns; i0 += 32 * kStep) {
     float w = 0.f;
-    if (i0 + lane < s.ns) {
-      const float2 ml = __ldcg(&ao.ml[part + (int64_t)(i0 + lane) * Rb]);
+    if (i0 + kStep * lane < ns) {
+      const float2 ml = __ldcg(&ao.ml[part + (int64_t)(i0 + kStep * lane) * Rb]);
       w = exp2f(ml.x - mu);
       l = fmaf(w, ml.y, l);
     }
-    const int n = min(32, s.ns - i0);
+    const int n = min(32, (ns - i0 + kStep - 1) / kStep);
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* from = ao.o + (part + (int64_t)(i0 + i) * Rb) * D + lane * E;
+      const float* from = ao.o + (part + (int64_t)(i0 + kStep * i) * Rb) * D + lane * E;
       float v[E];
       if constexpr (E == 4) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(from));
@@ -266,8 +273,19 @@ attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const At
     }
   }
   l = warp_sum(l);
+  if constexpr (kWide) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o[e] = (s_o[0][lane * E + e] + s_o[1][lane * E + e]) + (s_o[2][lane * E + e] + s_o[3][lane * E + e]);
+  }
   const int64_t tok = s.q0 + (row >> tb.g_shift);
-  const int head = (h << tb.g_shift) + (row & ((1 << tb.g_shift) - 1));
+  const int head = (int)(h << tb.g_shift) + (int)(row & ((1u << tb.g_shift) - 1));
   if (lane == 0 && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m + log2f(l));
   const float inv = 1.f / l;
   T* to = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D + lane * E;
@@ -290,25 +308,33 @@ cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendO
 
 template <typename T, int D>
 cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
+  const bool wide = n_rows <= 16 * 148;   // one wave of CTAs
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((n_rows + 3) / 4));
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3((unsigned)(wide ? n_rows : (n_rows + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D>, tb, n_rows, ao);
+  return wide ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D, true>, tb, n_rows, ao)
+              : cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D, false>, tb, n_rows, ao);
 }
 
 }  // namespace
 
-// bf16: 256 rows a block where some sequence has more than a tile of 128.
-// fp32: 64 rows, or 16 where no block has more to fill.
+// bf16: 256 rows a block where some sequence has more than a tile of 128.  A
+// tile takes about 2850 clocks; an item's queries, pipeline fill and output
+// 3.5 times that, a part of 256 rows (133 KB) and its merge 3 times.
+// fp32: 64 rows, or 16 where no block has more to fill.  A tile takes about
+// 8000 clocks (64 rows), the rest of an item half of that.
 AttendShape attend_shape(int dtype, int D, int most) {
-  if (dtype == WI_BF16) return AttendShape{most <= 128 ? 128 : 256, 128, 148};
-  return AttendShape{most <= 16 ? 16 : 64, D == 128 ? 32 : 64, most <= 16 ? 4 * 148 : 2 * 148};
+  if (dtype == WI_BF16) {
+    const int rows = most <= 128 ? 128 : 256;
+    return AttendShape{rows, 128, 148, 3.5, 3.0 * rows / 256};
+  }
+  return AttendShape{most <= 16 ? 16 : 64, D == 128 ? 32 : 64, most <= 16 ? 4 * 148 : (D == 128 ? 2 : 3) * 148, 0.5, 0.2};
 }
 
 cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {

@@ -34,10 +34,19 @@ __device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT)
   }
   const AttendSeq& s = tb.seq[lo];
   Item it;
-  const uint32_t ns = s.ns, x = item - s.item0, y = x / ns, split = x - y * ns;
-  const uint32_t up = y / (uint32_t)tb.hkv;
-  const int blk = s.nblk - 1 - (int)up, all = s.n << tb.g_shift;
-  it.h = (int)(y - up * tb.hkv);
+  const uint32_t ns = s.ns, x = item - s.item0, hkv = tb.hkv, nblk = s.nblk;
+  const int all = s.n << tb.g_shift;
+  uint32_t back, split = 0;   // blocks from the last
+  if (ns == 1) {
+    back = x / hkv;
+    it.h = (int)(x - back * hkv);
+  } else {   // the blocks that read a run of keys next to one another
+    const uint32_t y = x / nblk;
+    back = x - y * nblk;
+    split = y / hkv;
+    it.h = (int)(y - split * hkv);
+  }
+  const int blk = (int)(nblk - 1 - back);
   it.b = s.b; it.T = s.T; it.n = s.n; it.q0 = s.q0;
   it.row0 = blk * tb.rows;
   it.rows = min(tb.rows, all - it.row0);

@@ -231,16 +231,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const AppendA
 // -------------------------------------------------------------- attention
 // Key runs per block (ns).  Many blocks: one run each, and the item grid
 // fills the SMs.  Few: the key axis is split until the longest item and the
-// work per SM balance.  Costs are in key tiles; an item's fixed cost (its
-// queries, pipeline fill and output) and the merge are about two each.
-constexpr int kItemCost = 2, kMergeCost = 2, kMinTiles = 2, kMaxSplit = 148;
+// work per SM balance, in key tiles (attend_shape has the other costs).
+constexpr double kMergeCost = 2.0;   // the merge's launch
+constexpr int kMinTiles = 2, kMaxSplit = 148;
 
 int64_t tiles_of(const AttendSeq& s, int G, int R, int KT, int blk) {
   const int64_t rows = std::min<int64_t>((int64_t)(blk + 1) * R, (int64_t)s.n * G);
   return cdiv((int64_t)s.T - s.n + cdiv(rows, G), KT);
 }
 
-void choose_splits(AttendPlan& pl, int R, int KT, int slots) {
+void choose_splits(AttendPlan& pl, const AttendShape& sh) {
+  const int R = sh.rows, KT = sh.keys, slots = sh.slots;
   double total = 0;
   int64_t longest = 0;
   for (int i = 0; i < pl.n_seq; ++i) {
@@ -250,14 +251,18 @@ void choose_splits(AttendPlan& pl, int R, int KT, int slots) {
     longest = std::max(longest, most);
     s.ns = 1;
   }
-  if ((double)(longest + kItemCost) <= total / slots) return;   // enough blocks
+  if ((double)longest + sh.item_cost <= total / slots) return;   // enough blocks
   auto cost = [&](int64_t C) {
-    double items = 0;
-    for (int i = 0; i < pl.n_seq; ++i)
-      items += (double)pl.seq[i].nblk * pl.hkv * cdiv(tiles_of(pl.seq[i], pl.G, R, KT, pl.seq[i].nblk - 1), C);
-    const double one = (double)std::min(C, longest) + kItemCost;
-    const double t = items <= slots ? one : (total + items * kItemCost) / slots + 0.5 * one;
-    return t + (C < longest ? kMergeCost : 0);
+    double items = 0, parts = 0;   // parts in full blocks
+    for (int i = 0; i < pl.n_seq; ++i) {
+      const AttendSeq& s = pl.seq[i];
+      const double runs = (double)cdiv(tiles_of(s, pl.G, R, KT, s.nblk - 1), C);
+      items += s.nblk * pl.hkv * runs;
+      if (runs > 1) parts += pl.hkv * runs * std::min<double>((double)s.n * pl.G / R, s.nblk);
+    }
+    const double one = (double)std::min(C, longest) + sh.item_cost, spread = sh.part_cost * parts / slots;
+    const double t = items <= slots ? one : (total + items * sh.item_cost) / slots + 0.5 * one;
+    return t + spread + (C < longest ? kMergeCost : 0);
   };
   int64_t best = longest;
   double least = cost(longest);
@@ -307,7 +312,7 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
   pl.rows = sh.rows;
   int64_t items = 0;
   for (int i = 0; i < pl.n_seq; ++i) pl.seq[i].nblk = (int)cdiv((int64_t)pl.seq[i].n * G, sh.rows);
-  choose_splits(pl, sh.rows, sh.keys, sh.slots);
+  choose_splits(pl, sh);
   int64_t parts = 0, mrows = 0;
   for (int i = 0; i < pl.n_seq; ++i) {
     AttendSeq& s = pl.seq[i];

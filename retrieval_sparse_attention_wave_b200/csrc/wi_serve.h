@@ -29,7 +29,7 @@ struct AttendSeq {
   int32_t nblk;     // row blocks per unit
   int32_t ns;       // key runs per block
   int32_t item0;    // its first item: blocks descending (the longest key range
-                    // first), then KV heads, then runs
+                    // first), then KV heads; split, runs, KV heads, blocks
   int32_t part0;    // its first part row (ns > 1)
   int32_t mrow0;    // its first row of the merge kernel (ns > 1)
 };
@@ -54,9 +54,12 @@ struct AttendArgs {
 };
 
 // Rows per block, keys per tile and items running at once, for a call whose
-// blocks have at most `most` rows to fill (wi_attend.cu).
+// blocks have at most `most` rows to fill (wi_attend.cu); in times of a key
+// tile of a full block, what an item costs besides its tiles and what writing
+// and merging a full block's part costs.
 struct AttendShape {
   int rows, keys, slots;
+  double item_cost, part_cost;
 };
 AttendShape attend_shape(int dtype, int D, int most);
 cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s);
