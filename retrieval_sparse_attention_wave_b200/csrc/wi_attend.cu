@@ -31,7 +31,7 @@ struct FmaShape {
   static constexpr int CPT = D / 64;       // 16-byte output chunks per thread
   static constexpr int LD = D + 4;         // padded row: 8 rows on 8 different bank groups
   static constexpr int PLD = KT + 4;
-  static constexpr size_t kSmem = (size_t)(R * LD + 2 * KT * LD + R * PLD) * 4;
+  static constexpr size_t kSmem = (size_t)(R * LD + 2 * KT * LD + R * PLD) * 4 + 2 * KT * 8;
 };
 
 template <int D, int RT>
@@ -50,19 +50,37 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
   const int G = 1 << tb.g_shift;
   constexpr int CH = D / 4;   // 16-byte chunks of a row
 
-  // rows [base, base + KT) of a pool into a tile; rows behind key_end are zero
-  auto load_tile = [&](const Pool& p, float* dst, int base) {
-    for (int c = tid; c < S::KT * CH; c += 128) {
-      const int r = c / CH, ch = c % CH;
-      const int64_t row = base + r < it.key_end ? pool_row(p, tb.hkv, D, it.b, it.h, base + r, status) : -1;
-      float* to = dst + r * S::LD + ch * 4;
-      if (row >= 0) cp_async16(to, reinterpret_cast<const float*>(p.base) + row + ch * 4);
+  // Element offsets of a tile's rows in the pools (-1: no token's row), by a
+  // thread each, for two tiles; the page of the next one is looked up while a
+  // tile is worked on.
+  int64_t* srow = reinterpret_cast<int64_t*>(sp + S::R * S::PLD);
+  auto page_of = [&](int t) {
+    const int key = t * S::KT + tid;
+    return tid < S::KT && t < it.t1 && key < it.key_end
+               ? __ldg(kp.bt + (int64_t)it.b * kp.max_pages + (key >> kp.page_shift)) : -1;
+  };
+  auto set_rows = [&](int t, int page) {
+    const int key = t * S::KT + tid;
+    if (tid < S::KT && t < it.t1)
+      srow[(t & 1) * S::KT + tid] = key < it.key_end ? pool_row_pg(kp, tb.hkv, D, it.h, key, page, status) : -1;
+  };
+  // the rows of tile t from a pool into shared memory; zeros where there is none
+  auto load_tile = [&](const Pool& p, float* dst, int t) {
+    constexpr int kPerPass = 128 / CH;
+#pragma unroll 4
+    for (int r = tid / CH; r < S::KT; r += kPerPass) {
+      const int64_t row = srow[(t & 1) * S::KT + r];
+      float* to = dst + r * S::LD + (tid % CH) * 4;
+      if (row >= 0) cp_async16(to, reinterpret_cast<const float*>(p.base) + row + (tid % CH) * 4);
       else *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     cp_async_commit();
   };
 
-  if (it.t0 < it.t1) load_tile(kp, sk, it.t0 * S::KT);
+  int page = page_of(it.t0 + 1);
+  set_rows(it.t0, page_of(it.t0));
+  __syncthreads();
+  if (it.t0 < it.t1) load_tile(kp, sk, it.t0);
   for (int c = tid; c < S::R * CH; c += 128) {
     const int r = c / CH, ch = c % CH;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -88,7 +106,9 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
 
   for (int t = it.t0; t < it.t1; ++t) {
     const int base = t * S::KT;
-    load_tile(vp, sv, base);
+    load_tile(vp, sv, t);
+    set_rows(t + 1, page);
+    page = page_of(t + 2);
     cp_async_wait<1>();
     __syncthreads();
     float s[RT][S::KPT];
@@ -119,7 +139,7 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
         for (int j = 0; j < S::KPT; ++j) s[i][j] = a[i][j].x + a[i][j].y;
     }
     __syncthreads();   // the key tile is free
-    if (t + 1 < it.t1) load_tile(kp, sk, base + S::KT);
+    if (t + 1 < it.t1) load_tile(kp, sk, t + 1);
     else cp_async_commit();
     const bool diag = base + S::KT - 1 > first_pos;   // some row does not see all of the tile
     if (diag) {
@@ -327,14 +347,15 @@ cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao,
 // bf16: 256 rows a block where some sequence has more than a tile of 128.  A
 // tile takes about 2850 clocks; an item's queries, pipeline fill and output
 // 3.5 times that, a part of 256 rows (133 KB) and its merge 3 times.
-// fp32: 64 rows, or 16 where no block has more to fill.  A tile takes about
-// 8000 clocks (64 rows), the rest of an item half of that.
+// fp32: 64 rows, or 16 where no block has more to fill.  An item's fixed part
+// (about 5 us) is two tiles of 64 rows, or six of 16.
 AttendShape attend_shape(int dtype, int D, int most) {
   if (dtype == WI_BF16) {
     const int rows = most <= 128 ? 128 : 256;
     return AttendShape{rows, 128, 148, 3.5, 3.0 * rows / 256};
   }
-  return AttendShape{most <= 16 ? 16 : 64, D == 128 ? 32 : 64, most <= 16 ? 4 * 148 : (D == 128 ? 2 : 3) * 148, 0.5, 0.2};
+  if (most <= 16) return AttendShape{16, D == 128 ? 32 : 64, 4 * 148, 6.0, 1.0};
+  return AttendShape{64, D == 128 ? 32 : 64, (D == 128 ? 2 : 3) * 148, 2.0, 0.5};
 }
 
 cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
