@@ -351,6 +351,7 @@ cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao,
 // (about 5 us) is two tiles of 64 rows, or six of 16.
 AttendShape attend_shape(int dtype, int D, int most) {
   if (dtype == WI_BF16) {
+    if (most <= 16) return AttendShape{16, 128, 148, 2.0, 0.2};
     const int rows = most <= 128 ? 128 : 256;
     return AttendShape{rows, 128, 148, 3.5, 3.0 * rows / 256};
   }
@@ -366,7 +367,7 @@ cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_
                      reinterpret_cast<float*>(a.ws + pl.off_o), a.out_stride, pl.Hq};
   const bool wide = pl.D == 128;
   cudaError_t e;
-  if (pl.dtype == WI_BF16) e = launch_attend_umma(tb, pl, a, ao, s);
+  if (pl.dtype == WI_BF16) e = pl.rows == 16 ? launch_attend_few(tb, pl, a, ao, s) : launch_attend_umma(tb, pl, a, ao, s);
   else if (pl.rows == 16) e = wide ? launch_fma<128, 2>(tb, a, ao, s) : launch_fma<64, 2>(tb, a, ao, s);
   else e = wide ? launch_fma<128, 8>(tb, a, ao, s) : launch_fma<64, 8>(tb, a, ao, s);
   if (e != cudaSuccess || pl.n_merge_rows == 0) return e;

@@ -88,8 +88,11 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
-// bf16 blocks on the tensor cores (wi_attend_umma.cu)
+// bf16: blocks of 128 or 256 rows (wi_attend_umma.cu), and of 16
+// (wi_attend_few.cu)
 cudaError_t launch_attend_umma(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
                                const AttendOut& ao, cudaStream_t s);
+cudaError_t launch_attend_few(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
+                              const AttendOut& ao, cudaStream_t s);
 
 }  // namespace wi

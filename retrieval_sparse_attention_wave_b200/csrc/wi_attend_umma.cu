@@ -22,20 +22,14 @@
 // The output is rescaled only when a row's maximum rises by more than 2^8:
 // the reference point m only keeps the powers in range, P and the mass being
 // relative to the same m whatever it is.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <algorithm>
 #include <cmath>
-#include <mutex>
 
-#include "wi_attend.cuh"
+#include "wi_attend_tiles.cuh"
 #include "wi_umma.cuh"
 
 namespace wi {
 namespace {
 
-constexpr int kRows = 128;          // rows of a query tile, keys of a key tile
 constexpr int kUThreads = 384;
 constexpr float kRescale = 24.f;     // log2 of the growth that forces a rescale
 constexpr int kPoly = 4;            // every kPoly-th pair of weights without the special-function unit
@@ -60,27 +54,6 @@ __device__ __forceinline__ void tensor_load_3d(void* smem, const void* tmap, int
       "r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  const uint32_t b = smem_addr(bar);
-  if (try_bar(b, parity)) return true;
-#pragma unroll 1
-  for (uint32_t i = 0; i < kSpinLimit; ++i)
-    if (try_bar(b, parity)) return true;
-  atomicOr(status, WI_DEV_TIMEOUT);
-  return false;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 2^x without the special-function unit: x = n + f, |f| <= 1/2 (the sum with
 // 1.5 * 2^23 rounds x to the integer n, which is then in its low bits), 2^f
 // from a degree-5 polynomial (value 1 at 0, the others fitted for the least
@@ -134,13 +107,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r != 0;
 }
-// the largest of three, NaN if one is NaN
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kUThreads, 1)
 attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant__ CUtensorMap map_q,
@@ -200,79 +166,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           tensor_load_3d(sq + i * S::kTile + c * S::kBlock, &map_q, 64 * c, it.h * G,
                          it.q0 + ((it.row0 + i * kRows) >> tb.g_shift), &s_q);
     }
-    const int32_t* bt = kp.bt + (int64_t)it.b * kp.max_pages;
-    const int page_mask = (1 << kp.page_shift) - 1;
-    bool ok = true;
-    if (kp.page_shift >= 3) {
-      // a box of min(P, 128) rows per lane; rows no token has, or on a page
-      // outside the pool, are read outside the map, as zeros
-      const int r_shift = min(kp.page_shift, 7), per = kRows >> r_shift;
-      const int bx = lane & (per - 1), c = lane / per;
-      const int none = (int)((kp.n_pages * tb.hkv) << kp.page_shift);
-      auto page_at = [&](int t) {
-        const int key = t * kRows + (bx << r_shift);
-        return key < it.key_end && t < it.t1 ? __ldg(bt + (key >> kp.page_shift)) : -1;
-      };
-      int page = page_at(it.t0), issued = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int t = it.t0 + j, key = t * kRows + (bx << r_shift);
-        int y = none;
-        if (key < it.key_end) {
-          if (page >= 0 && page < kp.n_pages)
-            y = ((page * tb.hkv + it.h) << kp.page_shift) + (key & page_mask);
-          else
-            flag_error(status, WI_DEV_BAD_PAGE);
-        }
-        page = page_at(t + 1);
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int u = 2 * j + kv, st = u % S::kStages;
-          if (u >= S::kStages) ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect(&s_full[st], S::kTile);
-          __syncwarp();
-          if (c < S::kBlocks)
-            tensor_load_2d(ring + (size_t)st * S::kTile + c * S::kBlock + (bx << r_shift) * 128,
-                           kv ? &map_v : &map_k, 64 * c, y, &s_full[st]);
-          issued = u + 1;
-        }
-      }
-      if (!ok)   // a wait gave up: no copy is left in flight when the CTA ends
-        for (int u = max(0, issued - S::kStages); u < issued; ++u)
-          wait_bar(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
-    } else {
-      // pages of fewer than 8 rows: 16-byte copies into the swizzled layout,
-      // two units behind the one being issued
-      constexpr int CH = D / 8, kLag = 2;
-      auto arrive = [&](int u) {
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_full[u % S::kStages]);
-      };
-      int u = 0;
-      for (; u < 2 * n && ok; ++u) {
-        const int t = it.t0 + u / 2, st = u % S::kStages;
-        if (u >= S::kStages) ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / S::kStages - 1) & 1u, status));
-        if (!ok) break;
-        const Pool& p = u & 1 ? vp : kp;
-        unsigned char* dst = ring + (size_t)st * S::kTile;
-#pragma unroll 4
-        for (int i = lane; i < kRows * CH; i += 32) {
-          const int r = i / CH, ch = i % CH, key = t * kRows + r;
-          const int64_t row = key < it.key_end ? pool_row(p, tb.hkv, D, it.b, it.h, key, status) : -1;
-          unsigned char* to = dst + (ch >> 3) * S::kBlock + swz128(r, ch & 7);
-          if (row >= 0) cp_async16(to, reinterpret_cast<const T*>(p.base) + row + ch * 8);
-          else *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        cp_async_commit();
-        if (u >= kLag) {
-          cp_async_wait<kLag>();
-          arrive(u - kLag);
-        }
-      }
-      cp_async_wait<0>();
-      if (ok)
-        for (int v = max(0, u - kLag); v < u; ++v) arrive(v);
-    }
+    load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
   } else if (warp == 9 && n > 0) {
     // ----------------------------------------------------------------- MMAs
     // The whole warp runs the loop, so that addresses and descriptors stay in
@@ -572,30 +466,6 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   }
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point; null when
-// unavailable
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-bool encode(CUtensorMap* tm, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  const cuuint32_t one[3] = {1, 1, 1};
-  auto fn = encode_fn();
-  return fn && fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
                          cudaStream_t s) {
@@ -605,13 +475,7 @@ cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const Atte
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)pl.Hq, (cuuint64_t)pl.q_tokens};
   const cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
   const cuuint32_t qb[3] = {64, (cuuint32_t)pl.G, (cuuint32_t)(kRows / pl.G)};
-  // the pools as rows of D channels; page boxes of at most 128 rows (for
-  // pages of fewer than 8 rows the maps are not used)
-  const cuuint64_t pd[2] = {(cuuint64_t)D, (cuuint64_t)((a.kp.n_pages * pl.hkv) << a.kp.page_shift)};
-  const cuuint64_t ps[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t pb[2] = {64, (cuuint32_t)std::min(kRows, 1 << a.kp.page_shift)};
-  if (!encode(&mq, 3, a.q, qd, qs, qb) || !encode(&mk, 2, a.kp.base, pd, ps, pb) ||
-      !encode(&mv, 2, a.vp.base, pd, ps, pb))
+  if (!encode_map(&mq, 3, a.q, qd, qs, qb) || !encode_pools(&mk, &mv, a, pl.hkv, D))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attend_umma_kernel<D>>(S::kSmem);
   if (e != cudaSuccess) return e;
