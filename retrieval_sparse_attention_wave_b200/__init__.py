@@ -612,6 +612,12 @@ def _token_rows(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
     return row
 
 
+# The current stream's handle, without making a Stream object of it (3 us a
+# call) where torch has the accessor its own generated code uses.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _elsewhere(dev: int, stream):
     """The stream to make current for a call whose tensors are on `dev`, None
     when the current stream is the one to use (the common case)."""
@@ -709,7 +715,7 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
                    out.n_free.data_ptr(), out.starts.data_ptr(), capacity,
                    out.slot_map.data_ptr(), out.positions.data_ptr())
     _check(_lib.wi_plan_pages(C.byref(p), ws.data_ptr(), ws.numel(),
-                              torch.cuda.current_stream().cuda_stream), "wi_plan_pages")
+                              _current_stream(dev)), "wi_plan_pages")
     return out
 
 
@@ -740,7 +746,7 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
     a = WiKVAppend(_dtype_code(k_pool.dtype), n, H, d, P, n_pages, k.data_ptr(), v.data_ptr(),
                    ks, vs, slot_map.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
     _check(_lib.wi_append_kv(C.byref(a), ws.data_ptr(), ws.numel(),
-                             torch.cuda.current_stream().cuda_stream), "wi_append_kv")
+                             _current_stream(dev)), "wi_append_kv")
 
 
 @dataclass
@@ -812,7 +818,7 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     _on_gpu("ws", ws, torch.uint8, dev)
     c, p = kv.c_struct(), params.c_struct(qs, os_)
     _check(_lib.wi_attend(q.data_ptr(), C.byref(c), C.byref(p), out.data_ptr(), lse.data_ptr(),
-                          ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream),
+                          ws.data_ptr(), ws.numel(), _current_stream(dev)),
            "wi_attend")
     return out, lse
 

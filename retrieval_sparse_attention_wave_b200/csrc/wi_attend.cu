@@ -47,6 +47,7 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_launch_dependents();
   const Item it = item_of(tb, blockIdx.x, S::KT);
+  if (it.t0 == it.t1) return;
   const int G = 1 << tb.g_shift;
   constexpr int CH = D / 4;   // 16-byte chunks of a row
 
@@ -256,7 +257,10 @@ attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const At
   const uint32_t in = (uint32_t)(x - s.mrow0), h = in / all, row = in - h * all;
   const uint32_t blk = row / (uint32_t)tb.rows, rr = row - blk * tb.rows;
   const int64_t part = s.part0 + ((int64_t)blk * tb.hkv + h) * s.ns * Rb + rr;
-  const int ns = s.ns;
+  // its block's runs
+  const uint32_t last = min((blk + 1) * (uint32_t)tb.rows, all) - 1;
+  const uint32_t tiles = ((uint32_t)(s.T - s.n) + (last >> tb.g_shift) + tb.keys) / tb.keys;   // (of the keys its last row sees)
+  const int ns = (int)((tiles + s.run - 1) / s.run);
   pdl_wait();   // the parts are there
   if (x >= n_rows) return;
   float m = -INFINITY;
@@ -361,7 +365,7 @@ AttendShape attend_shape(int dtype, int D, int most) {
 
 cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
   AttendTable tb;
-  tb.n_seq = pl.n_seq; tb.n_items = pl.n_items; tb.hkv = pl.hkv; tb.g_shift = log2_of(pl.G); tb.rows = pl.rows;
+  tb.n_seq = pl.n_seq; tb.n_items = pl.n_items; tb.hkv = pl.hkv; tb.g_shift = log2_of(pl.G); tb.rows = pl.rows; tb.keys = pl.keys;
   std::copy(pl.seq, pl.seq + pl.n_seq, tb.seq);
   const AttendOut ao{a.out, a.lse, reinterpret_cast<float2*>(a.ws + pl.off_ml),
                      reinterpret_cast<float*>(a.ws + pl.off_o), a.out_stride, pl.Hq};

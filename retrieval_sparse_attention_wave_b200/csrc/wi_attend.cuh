@@ -12,7 +12,7 @@ namespace wi {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendTable {
-  int32_t n_seq, n_items, hkv, g_shift, rows;
+  int32_t n_seq, n_items, hkv, g_shift, rows, keys;   // (rows of a block, keys of a tile)
   AttendSeq seq[kMaxBatch];
 };
 
@@ -57,9 +57,8 @@ __device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT)
   it.t1 = (int)nt;
   it.part = -1;
   if (ns > 1) {
-    const uint32_t each = nt / ns, rest = nt - each * ns;   // the first `rest` runs take one more
-    it.t0 = (int)(each * split + min(rest, split));
-    it.t1 = it.t0 + (int)(each + (split < rest));
+    it.t0 = (int)min(nt, split * (uint32_t)s.run);
+    it.t1 = (int)min(nt, (split + 1) * (uint32_t)s.run);
     it.part = s.part0 + (((int64_t)blk * tb.hkv + it.h) * s.ns + split) * min(tb.rows, all);
   }
   return it;

@@ -51,6 +51,8 @@ attend_few_kernel(const __grid_constant__ AttendTable tb, const __nv_bfloat16* _
   __shared__ uint32_t s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   pdl_launch_dependents();
+  const Item it = item_of(tb, blockIdx.x, kRows);
+  if (it.t0 == it.t1) return;
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&s_full[i], 1);
@@ -59,12 +61,11 @@ attend_few_kernel(const __grid_constant__ AttendTable tb, const __nv_bfloat16* _
     mbar_init_fence();
     s_bad = 0;
   }
-  const Item it = item_of(tb, blockIdx.x, kRows);
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
   const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
   __syncthreads();
   if (warp == kFewWarps) {
-    if (n > 0) load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
+    load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
     return;
   }
 

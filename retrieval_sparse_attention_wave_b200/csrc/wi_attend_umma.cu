@@ -123,6 +123,8 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler)
   pdl_launch_dependents();
+  const Item it = item_of(tb, blockIdx.x, kRows);
+  if (it.t0 == it.t1) return;
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&s_full[i], 1);
@@ -147,7 +149,6 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   tc_fence_after();
   constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
 
-  const Item it = item_of(tb, blockIdx.x, kRows);
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
   const int nq = it.rows > kRows ? 2 : 1;
   const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
@@ -157,7 +158,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 8 && n > 0) {
+  if (warp == 8) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       mbar_arrive_expect(&s_q, (uint32_t)nq * S::kTile);
@@ -167,7 +168,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
                          it.q0 + ((it.row0 + i * kRows) >> tb.g_shift), &s_q);
     }
     load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
-  } else if (warp == 9 && n > 0) {
+  } else if (warp == 9) {
     // ----------------------------------------------------------------- MMAs
     // The whole warp runs the loop, so that addresses and descriptors stay in
     // uniform registers; one elected lane issues each batch.
@@ -242,7 +243,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
     if (elect_one()) umma_commit(&s_done);
     __syncwarp();
     wait_bar(&s_done, 0, status);
-  } else if (warp >= 10 && n > 0) {
+  } else if (warp >= 10) {
     // ------------------------------------------- value tiles on the diagonal
     for (int j = fix_from; j < n; ++j) {
       // (the ring's phase of V_j is known only from a permission in the MMA
@@ -384,7 +385,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
           mbar_arrive(&s_p[i][1]);
         }
       }
-      if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&s_o[i], (uint32_t)(n - 1) & 1u, status));
+      if (ok) ok = __all_sync(0xffffffffu, wait_bar(&s_o[i], (uint32_t)(n - 1) & 1u, status));
     }
     if (used) {
       tc_fence_after();
@@ -408,9 +409,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
 #pragma unroll 1
       for (int col = 0; col < D; col += 16) {
         uint32_t y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = 0u;
-        if (n > 0) tmem_ld16(to + col, y);
+        tmem_ld16(to + col, y);
         if (part) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);

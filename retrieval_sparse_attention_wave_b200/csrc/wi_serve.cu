@@ -250,13 +250,14 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
     total += 0.5 * (double)(most + least) * s.nblk * pl.hkv;
     longest = std::max(longest, most);
     s.ns = 1;
+    s.run = 0;
   }
   if ((double)longest + sh.item_cost <= total / slots) return;   // enough blocks
   auto cost = [&](int64_t C) {
     double items = 0, parts = 0;   // parts in full blocks
     for (int i = 0; i < pl.n_seq; ++i) {
       const AttendSeq& s = pl.seq[i];
-      const double runs = (double)cdiv(tiles_of(s, pl.G, R, KT, s.nblk - 1), C);
+      const double runs = 0.5 * (double)(cdiv(tiles_of(s, pl.G, R, KT, s.nblk - 1), C) + cdiv(tiles_of(s, pl.G, R, KT, 0), C));
       items += s.nblk * pl.hkv * runs;
       if (runs > 1) parts += pl.hkv * runs * std::min<double>((double)s.n * pl.G / R, s.nblk);
     }
@@ -274,7 +275,9 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   }
   for (int i = 0; i < pl.n_seq; ++i) {
     AttendSeq& s = pl.seq[i];
-    s.ns = (int)cdiv(tiles_of(s, pl.G, R, KT, s.nblk - 1), best);
+    const int64_t most = tiles_of(s, pl.G, R, KT, s.nblk - 1);
+    s.ns = (int)cdiv(most, best);
+    s.run = (int)cdiv(most, s.ns);
   }
 }
 
@@ -310,6 +313,7 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
                    [](const AttendSeq& x, const AttendSeq& y) { return x.T > y.T; });
   const AttendShape sh = attend_shape(pl.dtype, pl.D, most);
   pl.rows = sh.rows;
+  pl.keys = sh.keys;
   int64_t items = 0;
   for (int i = 0; i < pl.n_seq; ++i) pl.seq[i].nblk = (int)cdiv((int64_t)pl.seq[i].n * G, sh.rows);
   choose_splits(pl, sh);

@@ -20,14 +20,16 @@ wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int6
 // (token, head of the group) pairs of one KV head: row r of sequence b's unit
 // (b, h) is head h * G + r % G of the sequence's query token r / G.  An item
 // is a block of rows and a run of key tiles; a sequence with few blocks has
-// its key axis split into ns runs, whose parts a second kernel merges.
+// its key axis split into runs, whose parts a second kernel merges (the items
+// of runs that a block does not reach are empty and leave no part).
 struct AttendSeq {
   int32_t b;        // the sequence
   int32_t T;        // its tokens in the cache
   int32_t n;        // its query tokens
   int32_t q0;       // its first query token in the packed q
   int32_t nblk;     // row blocks per unit
-  int32_t ns;       // key runs per block
+  int32_t ns;       // key runs of the longest block
+  int32_t run;      // key tiles of a run (ns > 1; a block's last may be shorter)
   int32_t item0;    // its first item: blocks descending (the longest key range
                     // first), then KV heads; split, runs, KV heads, blocks
   int32_t part0;    // its first part row (ns > 1)
@@ -38,7 +40,7 @@ struct AttendPlan {
   int n_seq;        // sequences with query tokens, the longest key range first
   int n_items, n_merge_rows;
   int hkv, G, Hq, D, dtype;
-  int rows;         // rows per block
+  int rows, keys;   // rows per block, keys per tile
   int64_t q_tokens; // rows of the packed q
   size_t off_ml, off_o, total;   // workspace: {m, l} and o of the part rows
   AttendSeq seq[kMaxBatch];
