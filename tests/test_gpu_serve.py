@@ -344,6 +344,133 @@ def test_attend_on_another_stream_and_captured():
         W.attend(q, kv, params, ws=W.workspace(256, DEV))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 64, 1024])
+@pytest.mark.parametrize("G,q_lens", [(1, [16, 1, 9]), (8, [2, 1, 0]), (4, [4, 3, 1])])
+def test_attend_few_rows_page_sizes(dtype, page, G, q_lens):
+    """Blocks of at most 16 rows, full ones among them."""
+    kv = make_cache([1300, 128, 333], 2, 128, page, dtype, page + G)
+    check_attend(kv, make_q(sum(q_lens), 2 * G, 128, dtype, page), q_lens)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 127, 128, 129, 255, 257])
+def test_attend_one_token_at_every_edge_of_a_tile(dtype, d, T):
+    kv = make_cache([T, T + 1000], 2, d, 16, dtype, T)
+    check_attend(kv, make_q(2, 4, d, dtype, T), [1, 1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [40, 1500, 1536])
+def test_attend_later_keys_have_no_effect_on_few_rows(dtype, bad, T):
+    kv = make_cache([T], 2, 64, 16, dtype, 21)
+    q = make_q(6, 4, 64, dtype, 21)
+    clean, clean_lse = W.attend(q, kv, W.AttendParams(4, [6]))
+    at = T - 3
+    page, row = int(kv.block_table[0, at // 16]), at % 16
+    kv.v_pool[page, 0, row, 5] = bad
+    kv.k_pool[page, 1, row] = float("nan")
+    out, lse = W.attend(q, kv, W.AttendParams(4, [6]))
+    assert torch.equal(out[:3], clean[:3]) and torch.equal(lse[:3], clean_lse[:3])
+    hit = out[3:, :2, 5]
+    assert (hit == bad).all() if bad == bad else torch.isnan(hit).all()
+    assert torch.equal(out[:, :2, 6:], clean[:, :2, 6:]) and torch.equal(lse[:, :2], clean_lse[:, :2])
+    assert torch.isnan(out[3:, 2:]).all() and torch.isnan(lse[3:, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_full_batch(dtype):
+    rng = np.random.default_rng(23)
+    lens = rng.integers(1, 260, 256).tolist()
+    q_lens = [int(rng.integers(0, min(T, 40) + 1)) for T in lens]
+    kv = make_cache(lens, 1, 64, 16, dtype, 23)
+    check_attend(kv, make_q(sum(q_lens), 2, 64, dtype, 23), q_lens)
+    check_attend(kv, make_q(256, 2, 64, dtype, 24), [1] * 256)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_past_32_bits(dtype):
+    """A pool of more than 2^32 elements: rows appended to and attended on its
+    last pages."""
+    H, page, d, lens = 8, 16, 128, [700, 33]
+    n_pages = 2 ** 32 // (H * page * d) + 64
+    pools = torch.empty(2, n_pages, H, page, d, dtype=dtype, device=DEV)
+    need = [-(-T // page) for T in lens]
+    bt = torch.full((2, max(need)), -1, dtype=torch.int32)
+    last = torch.arange(n_pages - sum(need), n_pages, dtype=torch.int32).flip(0)
+    bt[0], bt[1, :need[1]] = last[:need[0]], last[need[0]:]
+    kv = W.KVCache(pools[0], pools[1], bt.to(DEV), lens)
+    k, v = make_q(sum(lens), H, d, dtype, 50), make_q(sum(lens), H, d, dtype, 51)
+    pos = torch.cat([torch.arange(T) for T in lens])
+    req = torch.repeat_interleave(torch.arange(2), torch.tensor(lens))
+    slots = (bt[req, pos // page] * page + pos % page).to(torch.int32).to(DEV)
+    W.append_kv(k, v, slots, pools[0], pools[1])
+    # the same rows in a small pool
+    small = torch.zeros(2, sum(need), H, page, d, dtype=dtype, device=DEV)
+    tail = int(n_pages - sum(need))
+    for q_lens in ([5, 33], [1, 1]):
+        q = make_q(sum(q_lens), 16, d, dtype, 52)
+        out, lse = W.attend(q, kv, W.AttendParams(16, q_lens))
+        small.copy_(pools[:, tail:])
+        near = W.KVCache(small[0], small[1], torch.where(bt >= 0, bt - tail, bt).to(DEV), lens)
+        want, want_lse = W.attend(q, near, W.AttendParams(16, q_lens))
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert torch.equal(pools[0, int(bt[0, 3]), :, 7], k[3 * page + 7])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_captured_single_tokens_share_a_workspace(dtype):
+    """Two graphs of split calls of other sizes on one workspace, replayed in
+    turns."""
+    caches = [make_cache([6000, 800], 2, 128, 16, dtype, 25), make_cache([300, 9000, 5], 2, 128, 16, dtype, 26)]
+    params = [W.AttendParams(8, [1, 1]), W.AttendParams(8, [1, 1, 1])]
+    ws = W.workspace(max(W.attend_workspace_bytes(c, p) for c, p in zip(caches, params)), DEV)
+    ws[256:].fill_(255)
+    graphs, outs = [], []
+    for i, (kv, p) in enumerate(zip(caches, params)):
+        q = make_q(len(kv.seq_lens), 8, 128, dtype, 27 + i)
+        want = W.attend(q, kv, p)
+        into = [torch.zeros_like(x) for x in want]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            W.attend(q, kv, p, out=into[0], lse=into[1], ws=ws)
+        graphs.append((g, q))
+        outs.append((want, into))
+    for _ in range(3):
+        for (g, _), (want, into) in zip(graphs, outs):
+            into[0].zero_()
+            g.replay()
+            assert torch.equal(into[0], want[0]) and torch.equal(into[1], want[1])
+
+
+def test_plan_and_append_on_another_stream():
+    side = torch.cuda.Stream()
+    table = make_table([30, 0, 17], 16, 40, 8, 27)
+    pools = torch.zeros(2, 40, 2, 16, 64, device=DEV)
+    k = torch.randn(6, 2, 64, device=DEV)
+    torch.cuda.synchronize()
+    plan = W.plan_pages(table, i32([3, 1, 2]), 6, update=True, stream=side)
+    W.append_kv(k, 2 * k, plan.slot_map, pools[0], pools[1], stream=side)
+    side.synchronize()
+    assert table.seq_lens.tolist() == [33, 1, 19]
+    for i, s in enumerate(plan.slot_map.tolist()):
+        assert torch.equal(pools[0, s // 16, :, s % 16], k[i])
+        assert torch.equal(pools[1, s // 16, :, s % 16], 2 * k[i])
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_tensors_on_another_device_than_the_current_one():
+    kv0 = make_cache([500, 3], 2, 64, 16, BF16, 29)
+    q = make_q(503, 4, 64, BF16, 29)
+    want, _ = W.attend(q, kv0, W.AttendParams(4))
+    kv1 = W.KVCache(*(x.to("cuda:1") for x in (kv0.k_pool, kv0.v_pool, kv0.block_table)), [500, 3])
+    out, _ = W.attend(q.to("cuda:1"), kv1, W.AttendParams(4))
+    assert out.device.index == 1 and torch.equal(out.to(DEV), want)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
