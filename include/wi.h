@@ -393,7 +393,9 @@ const char *wi_decode_stage_name(int32_t i);
  * tokens go to, their key and value rows written there, and their attention
  * over the cache (a prompt, a chunk of one, or single tokens that no index
  * covers yet).  Page-centred tensors with index pointers are the layout of
- * Vortex 2.B (vTensor); the calls are this library's own.
+ * Vortex 2.B (vTensor); the calls are this library's own.  As everywhere, a
+ * workspace serves one call at a time: calls that may overlap on the GPU
+ * (other streams, graphs replayed side by side) need one each.
  */
 
 /*
@@ -482,7 +484,11 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * Keys behind a query's position have no effect on it, whatever they hold
  * (NaN and infinities too), nor have pool rows behind T_b.  bf16 rounds the
  * softmax weights to bf16 for the product with the values; their sum and the
- * accumulators are fp32.
+ * accumulators are fp32.  A block-table entry outside the pool reads as zero
+ * rows and sets WI_DEV_BAD_PAGE.  Sequences with few query rows have their
+ * keys split over the SMs and joined in a fixed order: results do not change
+ * from run to run.  Workspace: wi_attend_workspace_size for the same cache
+ * and parameters.
  */
 typedef struct wi_attend_params {
   int32_t n_q_heads;           /* Hq, a multiple of Hkv with G in {1,2,4,8}     */

@@ -9,7 +9,9 @@
 // the end.  A tile costs a warp about 250 instructions, a third of the time
 // its 64 KB take to arrive, and a stage is free as soon as eight warps have
 // read it: the tensor-memory kernel holds its stages through a softmax of 128
-// rows, which leaves 96 KB in flight and 4.9 TB/s.
+// rows, which leaves 96 KB in flight and 4.9 TB/s.  16 tokens over 32768 keys
+// each, 8 KV heads of 128: 328 us, 6.5 TB/s; one over 131072: 82 us and a
+// merge of 6.
 #include <cmath>
 
 #include "wi_attend_tiles.cuh"
