@@ -691,29 +691,42 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
             return plan_pages(table, new_lens, capacity, out, update, ws)
     _need(bt.dim() == 2, "block_table: [batch][max_pages] is expected")
     i32, (B, max_pages) = torch.int32, bt.shape
-    _on_gpu("block_table", bt, i32, dev)
-    _on_gpu("seq_lens", table.seq_lens, i32, dev, (B,))
-    _on_gpu("new_lens", new_lens, i32, dev, (B,))
-    _on_gpu("free_pages", table.free_pages, i32, dev)
-    _on_gpu("n_free", table.n_free, i32, dev, (1,))
+    sl, free, n_free = table.seq_lens, table.free_pages, table.n_free
     if out is None:
         out = PagePlan.empty(table, capacity, update)
-    else:
-        _need(not update or (out.seq_lens is table.seq_lens and out.n_free is table.n_free),
-              "update: `out` must hold the table's own seq_lens and n_free")
-        _on_gpu("out.slot_map", out.slot_map, i32, dev, (capacity,))
-        _on_gpu("out.positions", out.positions, i32, dev, (capacity,))
-        _on_gpu("out.starts", out.starts, i32, dev, (B + 1,))
-        _on_gpu("out.seq_lens", out.seq_lens, i32, dev, (B,))
-        _on_gpu("out.n_free", out.n_free, i32, dev, (1,))
+    elif update and (out.seq_lens is not sl or out.n_free is not n_free):
+        raise ValueError("update: `out` must hold the table's own seq_lens and n_free")
+    slots, positions, starts, sl_out, n_free_out = (out.slot_map, out.positions, out.starts,
+                                                    out.seq_lens, out.n_free)
     if ws is None:
         ws = serve_workspace(bt.device)
-    _on_gpu("ws", ws, torch.uint8, dev)
-    p = WiPagePlan(B, table.page_size, table.n_pages, table.seq_lens.data_ptr(),
-                   new_lens.data_ptr(), bt.data_ptr(), max_pages, table.free_pages.data_ptr(),
-                   table.free_pages.numel(), table.n_free.data_ptr(), out.seq_lens.data_ptr(),
-                   out.n_free.data_ptr(), out.starts.data_ptr(), capacity,
-                   out.slot_map.data_ptr(), out.positions.data_ptr())
+    # one expression on the way of a call that is right (2 us less a call);
+    # the checks that name the argument otherwise
+    if not (bt.dtype is sl.dtype is new_lens.dtype is free.dtype is n_free.dtype is slots.dtype
+            is positions.dtype is starts.dtype is sl_out.dtype is n_free_out.dtype is i32
+            and ws.dtype is torch.uint8
+            and dev == sl.get_device() == new_lens.get_device() == free.get_device()
+            == n_free.get_device() == slots.get_device() == positions.get_device()
+            == starts.get_device() == sl_out.get_device() == n_free_out.get_device()
+            == ws.get_device()
+            and sl.numel() == new_lens.numel() == sl_out.numel() == B and starts.numel() == B + 1
+            and slots.numel() == positions.numel() == capacity
+            and n_free.numel() == n_free_out.numel() == 1
+            and bt.is_contiguous() and sl.is_contiguous() and new_lens.is_contiguous()
+            and free.is_contiguous() and slots.is_contiguous() and positions.is_contiguous()
+            and starts.is_contiguous() and sl_out.is_contiguous() and ws.is_contiguous()):
+        for name, t, shape in (("block_table", bt, (B, max_pages)), ("seq_lens", sl, (B,)),
+                               ("new_lens", new_lens, (B,)), ("free_pages", free, free.shape),
+                               ("n_free", n_free, (1,)), ("out.slot_map", slots, (capacity,)),
+                               ("out.positions", positions, (capacity,)),
+                               ("out.starts", starts, (B + 1,)), ("out.seq_lens", sl_out, (B,)),
+                               ("out.n_free", n_free_out, (1,))):
+            _on_gpu(name, t, i32, dev, shape)
+        _on_gpu("ws", ws, torch.uint8, dev)
+    p = WiPagePlan(B, table.page_size, table.n_pages, sl.data_ptr(), new_lens.data_ptr(),
+                   bt.data_ptr(), max_pages, free.data_ptr(), free.numel(), n_free.data_ptr(),
+                   sl_out.data_ptr(), n_free_out.data_ptr(), starts.data_ptr(), capacity,
+                   slots.data_ptr(), positions.data_ptr())
     _check(_lib.wi_plan_pages(C.byref(p), ws.data_ptr(), ws.numel(),
                               _current_stream(dev)), "wi_plan_pages")
     return out
@@ -732,8 +745,10 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
     _need(k_pool.dim() == 4 and k_pool.shape == v_pool.shape,
           "k_pool, v_pool: equal [n_pages][n_kv_heads][page_size][head_dim] shapes are expected")
     _device_of("k_pool", k_pool)
-    _on_gpu("k_pool", k_pool, k_pool.dtype, dev)
-    _on_gpu("v_pool", v_pool, k_pool.dtype, dev)
+    if not (k_pool.is_contiguous() and v_pool.is_contiguous() and v_pool.get_device() == dev
+            and v_pool.dtype is k_pool.dtype):
+        _on_gpu("k_pool", k_pool, k_pool.dtype, dev)
+        _on_gpu("v_pool", v_pool, k_pool.dtype, dev)
     n_pages, H, P, d = k_pool.shape
     ks, vs = _token_rows("k", k, k_pool), _token_rows("v", v, k_pool)
     n = k.shape[0]
@@ -803,9 +818,13 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     _need(kv.v_pool.shape == kp.shape and kv.block_table.dim() == 2
           and kv.block_table.shape[0] == len(kv.seq_lens), "kv: pools and table do not match")
     _device_of("k_pool", kp)
-    _on_gpu("k_pool", kp, kp.dtype, dev)
-    _on_gpu("v_pool", kv.v_pool, kp.dtype, dev)
-    _on_gpu("block_table", kv.block_table, torch.int32, dev)
+    vp, bt = kv.v_pool, kv.block_table
+    if not (kp.is_contiguous() and vp.is_contiguous() and bt.is_contiguous()
+            and dev == vp.get_device() == bt.get_device() and vp.dtype is kp.dtype
+            and bt.dtype is torch.int32):
+        _on_gpu("k_pool", kp, kp.dtype, dev)
+        _on_gpu("v_pool", vp, kp.dtype, dev)
+        _on_gpu("block_table", bt, torch.int32, dev)
     if out is None:
         out = torch.empty(n, Hq, d, dtype=q.dtype, device=q.device)
     os_ = _token_rows("out", out, kp)
