@@ -329,26 +329,17 @@ cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendO
   using S = FmaShape<D, RT>;
   const cudaError_t e = allow_smem<attend_fma_kernel<D, RT>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  attend_fma_kernel<D, RT><<<tb.n_items, S::kThreads, S::kSmem, s>>>(
-      tb, static_cast<const float*>(a.q), a.q_stride, a.kp, a.vp, ao, kLog2e / std::sqrt((float)D),
-      reinterpret_cast<uint32_t*>(a.ws));
-  return cudaGetLastError();
+  return launch_kernel(attend_fma_kernel<D, RT>, dim3(tb.n_items), S::kThreads, S::kSmem, s, false, tb,
+                       static_cast<const float*>(a.q), a.q_stride, a.kp, a.vp, ao, kLog2e / std::sqrt((float)D),
+                       reinterpret_cast<uint32_t*>(a.ws));
 }
 
 template <typename T, int D>
 cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
   const bool wide = n_rows <= 16 * 148;   // one wave of CTAs
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(wide ? n_rows : (n_rows + kMergeWarps - 1) / kMergeWarps));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D, true>, tb, n_rows, ao)
-              : cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D, false>, tb, n_rows, ao);
+  const dim3 grid((unsigned)(wide ? n_rows : (n_rows + kMergeWarps - 1) / kMergeWarps));
+  return launch_kernel(wide ? attend_merge_kernel<T, D, true> : attend_merge_kernel<T, D, false>, grid,
+                       32 * kMergeWarps, 0, s, true, tb, n_rows, ao);
 }
 
 }  // namespace

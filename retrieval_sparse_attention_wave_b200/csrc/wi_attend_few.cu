@@ -266,10 +266,9 @@ cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const Atte
   if (!encode_pools(&mk, &mv, a, pl.hkv, D)) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attend_few_kernel<D>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  attend_few_kernel<D><<<tb.n_items, kFewThreads, S::kSmem, s>>>(
-      tb, static_cast<const __nv_bfloat16*>(a.q), a.q_stride, mk, mv, a.kp, a.vp, ao,
-      kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
-  return cudaGetLastError();
+  return launch_kernel(attend_few_kernel<D>, dim3(tb.n_items), kFewThreads, S::kSmem, s, false, tb,
+                       static_cast<const __nv_bfloat16*>(a.q), a.q_stride, mk, mv, a.kp, a.vp, ao,
+                       kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
 }
 
 }  // namespace

@@ -491,9 +491,8 @@ cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const Atte
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<attend_umma_kernel<D>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  attend_umma_kernel<D><<<tb.n_items, kUThreads, S::kSmem, s>>>(
-      tb, mq, mk, mv, a.kp, a.vp, ao, kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
-  return cudaGetLastError();
+  return launch_kernel(attend_umma_kernel<D>, dim3(tb.n_items), kUThreads, S::kSmem, s, false, tb, mq, mk, mv, a.kp,
+                       a.vp, ao, kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
 }
 
 }  // namespace

@@ -247,11 +247,13 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   const int R = sh.rows, KT = sh.keys, slots = sh.slots;
   double total = 0;
   int64_t longest = 0;
+  int32_t most[kMaxBatch], least[kMaxBatch];   // tiles of a sequence's last and first block
   for (int i = 0; i < pl.n_seq; ++i) {
     AttendSeq& s = pl.seq[i];
-    const int64_t most = tiles_of(s, pl.G, R, KT, s.nblk - 1), least = tiles_of(s, pl.G, R, KT, 0);
-    total += 0.5 * (double)(most + least) * s.nblk * pl.hkv;
-    longest = std::max(longest, most);
+    most[i] = (int32_t)tiles_of(s, pl.G, R, KT, s.nblk - 1);
+    least[i] = (int32_t)tiles_of(s, pl.G, R, KT, 0);
+    total += 0.5 * ((double)most[i] + least[i]) * s.nblk * pl.hkv;
+    longest = std::max<int64_t>(longest, most[i]);
     s.ns = 1;
     s.run = 0;
   }
@@ -260,7 +262,7 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
     double items = 0, parts = 0;   // parts in full blocks
     for (int i = 0; i < pl.n_seq; ++i) {
       const AttendSeq& s = pl.seq[i];
-      const double runs = 0.5 * (double)(cdiv(tiles_of(s, pl.G, R, KT, s.nblk - 1), C) + cdiv(tiles_of(s, pl.G, R, KT, 0), C));
+      const double runs = 0.5 * (double)(cdiv(most[i], C) + cdiv(least[i], C));
       items += s.nblk * pl.hkv * runs;
       if (runs > 1) parts += pl.hkv * runs * std::min<double>((double)s.n * pl.G / R, s.nblk);
     }
@@ -269,18 +271,18 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
     return t + spread + (C < longest ? kMergeCost : 0);
   };
   int64_t best = longest;
-  double least = cost(longest);
-  for (int k = 2; k <= kMaxSplit; ++k) {
+  double cheapest = cost(longest);
+  // (fewer candidates with many sequences: 17 for 256 of them)
+  for (int k = 2; k <= kMaxSplit; k += 1 + k * pl.n_seq / 1024) {
     const int64_t C = cdiv(longest, k);
     if (C < kMinTiles) break;
     const double c = cost(C);
-    if (c < least) { least = c; best = C; }
+    if (c < cheapest) { cheapest = c; best = C; }
   }
   for (int i = 0; i < pl.n_seq; ++i) {
     AttendSeq& s = pl.seq[i];
-    const int64_t most = tiles_of(s, pl.G, R, KT, s.nblk - 1);
-    s.ns = (int)cdiv(most, best);
-    s.run = (int)cdiv(most, s.ns);
+    s.ns = (int)cdiv(most[i], best);
+    s.run = (int)cdiv(most[i], s.ns);
   }
 }
 
@@ -356,8 +358,7 @@ cudaError_t launch_plan_pages(const wi_page_plan& p, unsigned char* ws, cudaStre
              p.n_free, p.block_table, p.seq_lens_out, p.n_free_out, p.starts, p.slot_map, p.positions,
              reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 64)};
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(p.capacity, kPlanTokens), 4 * 148));
-  plan_pages_kernel<<<grid, kPlanThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(plan_pages_kernel, dim3(grid), kPlanThreads, 0, s, false, a);
 }
 
 cudaError_t launch_append_kv(const wi_kv_append& p, unsigned char* ws, cudaStream_t s) {
@@ -369,8 +370,7 @@ cudaError_t launch_append_kv(const wi_kv_append& p, unsigned char* ws, cudaStrea
                (int64_t)p.n_tokens * p.n_kv_heads * per_row, p.n_pages * p.page_size, p.n_kv_heads,
                ilog2(per_row), ilog2(p.page_size), reinterpret_cast<uint32_t*>(ws)};
   const int64_t grid = cdiv(a.n_chunks, kAppendThreads * kAppendBatch);
-  append_kv_kernel<<<dim3((unsigned)grid, 2), kAppendThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(append_kv_kernel, dim3((unsigned)grid, 2), kAppendThreads, 0, s, false, a);
 }
 
 }  // namespace wi

@@ -15,6 +15,24 @@ wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int6
                        const void* kp, const void* vp, const int32_t* bt, int max_pages,
                        const int32_t* seq_lens);
 
+// A launch whose error is its own (cudaGetLastError after <<<>>> would also
+// hand back what an earlier call of this thread left).
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
+                          bool behind_previous, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind_previous ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 // ---------------------------------------------------------------- attention
 // The query heads of a KV head share its keys, so the rows of a work item are
 // (token, head of the group) pairs of one KV head: row r of sequence b's unit
