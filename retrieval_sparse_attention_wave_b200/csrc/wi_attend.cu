@@ -39,9 +39,9 @@ struct FmaShape {
   static constexpr size_t kSmem = (size_t)(R * LD + 2 * KT * LD + R * PLD) * 4 + 2 * KT * 8;
 };
 
-template <int D, int RT>
+template <int D, int RT, int N>
 __global__ void __launch_bounds__(128)
-attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restrict__ q_, int64_t q_stride,
+attend_fma_kernel(const __grid_constant__ AttendTable<N> tb, const float* __restrict__ q_, int64_t q_stride,
                   const Pool kp, const Pool vp, const AttendOut ao, float scale, uint32_t* status) {
   using S = FmaShape<D, RT>;
   extern __shared__ __align__(16) float sh_fma[];
@@ -244,9 +244,9 @@ attend_fma_kernel(const __grid_constant__ AttendTable tb, const float* __restric
 // every fourth part and add up in a fixed order.
 constexpr int kMergeWarps = 4;
 
-template <typename T, int D, bool kWide>
+template <typename T, int D, bool kWide, int N>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const AttendOut ao) {
+attend_merge_kernel(const __grid_constant__ AttendTable<N> tb, int n_rows, const AttendOut ao) {
   constexpr int E = D / 32;   // columns per lane
   constexpr int kStep = kWide ? kMergeWarps : 1;
   __shared__ float s_o[kWide ? kMergeWarps : 1][D], s_l[kMergeWarps];
@@ -324,21 +324,21 @@ attend_merge_kernel(const __grid_constant__ AttendTable tb, int n_rows, const At
 
 inline int log2_of(int x) { int r = 0; while ((1 << r) < x) ++r; return r; }
 
-template <int D, int RT>
-cudaError_t launch_fma(const AttendTable& tb, const AttendArgs& a, const AttendOut& ao, cudaStream_t s) {
+template <int D, int RT, int N>
+cudaError_t launch_fma(const AttendTable<N>& tb, const AttendArgs& a, const AttendOut& ao, cudaStream_t s) {
   using S = FmaShape<D, RT>;
-  const cudaError_t e = allow_smem<attend_fma_kernel<D, RT>>(S::kSmem);
+  const cudaError_t e = allow_smem<attend_fma_kernel<D, RT, N>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_fma_kernel<D, RT>, dim3(tb.n_items), S::kThreads, S::kSmem, s, false, tb,
+  return launch_kernel(attend_fma_kernel<D, RT, N>, dim3(tb.n_items), S::kThreads, S::kSmem, s, false, tb,
                        static_cast<const float*>(a.q), a.q_stride, a.kp, a.vp, ao, kLog2e / std::sqrt((float)D),
                        reinterpret_cast<uint32_t*>(a.ws));
 }
 
-template <typename T, int D>
-cudaError_t launch_merge(const AttendTable& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
+template <typename T, int D, int N>
+cudaError_t launch_merge(const AttendTable<N>& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
   const bool wide = n_rows <= 16 * 148;   // one wave of CTAs
   const dim3 grid((unsigned)(wide ? n_rows : (n_rows + kMergeWarps - 1) / kMergeWarps));
-  return launch_kernel(wide ? attend_merge_kernel<T, D, true> : attend_merge_kernel<T, D, false>, grid,
+  return launch_kernel(wide ? attend_merge_kernel<T, D, true, N> : attend_merge_kernel<T, D, false, N>, grid,
                        32 * kMergeWarps, 0, s, true, tb, n_rows, ao);
 }
 
@@ -359,15 +359,20 @@ AttendShape attend_shape(int dtype, int D, int most) {
   return AttendShape{64, D == 128 ? 32 : 64, (D == 128 ? 2 : 3) * 148, 2.0, 0.5};
 }
 
-cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
-  AttendTable tb;
-  tb.n_seq = pl.n_seq; tb.n_items = pl.n_items; tb.hkv = pl.hkv; tb.g_shift = log2_of(pl.G); tb.rows = pl.rows; tb.keys = pl.keys;
+namespace {
+
+template <int N>
+cudaError_t launch_with(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
+  AttendTable<N> tb;
+  tb.n_seq = pl.n_seq; tb.n_items = pl.n_items; tb.hkv = pl.hkv;
+  tb.g_shift = log2_of(pl.G); tb.rows = pl.rows; tb.keys = pl.keys;
   std::copy(pl.seq, pl.seq + pl.n_seq, tb.seq);
   const AttendOut ao{a.out, a.lse, reinterpret_cast<float2*>(a.ws + pl.off_ml),
                      reinterpret_cast<float*>(a.ws + pl.off_o), a.out_stride, pl.Hq};
   const bool wide = pl.D == 128;
   cudaError_t e;
-  if (pl.dtype == WI_BF16) e = pl.rows == 16 ? launch_attend_few(tb, pl, a, ao, s) : launch_attend_umma(tb, pl, a, ao, s);
+  if (pl.dtype == WI_BF16)
+    e = pl.rows == 16 ? launch_attend_few(tb, pl, a, ao, s) : launch_attend_umma(tb, pl, a, ao, s);
   else if (pl.rows == 16) e = wide ? launch_fma<128, 2>(tb, a, ao, s) : launch_fma<64, 2>(tb, a, ao, s);
   else e = wide ? launch_fma<128, 8>(tb, a, ao, s) : launch_fma<64, 8>(tb, a, ao, s);
   if (e != cudaSuccess || pl.n_merge_rows == 0) return e;
@@ -376,6 +381,12 @@ cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_
                 : launch_merge<__nv_bfloat16, 64>(tb, pl.n_merge_rows, ao, s);
   return wide ? launch_merge<float, 128>(tb, pl.n_merge_rows, ao, s)
               : launch_merge<float, 64>(tb, pl.n_merge_rows, ao, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s) {
+  return pl.n_seq <= kFewSeqs ? launch_with<kFewSeqs>(pl, a, s) : launch_with<kMaxBatch>(pl, a, s);
 }
 
 }  // namespace wi

@@ -11,9 +11,14 @@ namespace wi {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The sequences of a call, a kernel parameter: 10 KB for the largest batch,
+// which takes 5 us more to launch, so the kernels are compiled for few
+// sequences as well.
+constexpr int kFewSeqs = 16;
+template <int N>
 struct AttendTable {
   int32_t n_seq, n_items, hkv, g_shift, rows, keys;   // (rows of a block, keys of a tile)
-  AttendSeq seq[kMaxBatch];
+  AttendSeq seq[N];
 };
 
 // One item of the plan, as its CTA needs it.
@@ -26,7 +31,8 @@ struct Item {
   int64_t part;         // first part row, -1: the whole key range
 };
 
-__device__ __forceinline__ Item item_of(const AttendTable& tb, int item, int KT) {
+template <int N>
+__device__ __forceinline__ Item item_of(const AttendTable<N>& tb, int item, int KT) {
   int lo = 0, hi = tb.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -89,9 +95,11 @@ cudaError_t allow_smem(size_t bytes) {
 
 // bf16: blocks of 128 or 256 rows (wi_attend_umma.cu), and of 16
 // (wi_attend_few.cu)
-cudaError_t launch_attend_umma(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
+template <int N>
+cudaError_t launch_attend_umma(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a,
                                const AttendOut& ao, cudaStream_t s);
-cudaError_t launch_attend_few(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
+template <int N>
+cudaError_t launch_attend_few(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a,
                               const AttendOut& ao, cudaStream_t s);
 
 }  // namespace wi

@@ -40,9 +40,9 @@ __device__ __forceinline__ uint32_t clean(uint32_t w, int key, int first_pos, in
   return w;
 }
 
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(kFewThreads, 1)
-attend_few_kernel(const __grid_constant__ AttendTable tb, const __nv_bfloat16* __restrict__ q, int64_t q_stride,
+attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16* __restrict__ q, int64_t q_stride,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const Pool kp, const Pool vp, const AttendOut ao, float scale, uint32_t* status) {
   using S = FewShape<D>;
@@ -258,24 +258,29 @@ attend_few_kernel(const __grid_constant__ AttendTable tb, const __nv_bfloat16* _
   }
 }
 
-template <int D>
-cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
+template <int D, int N>
+cudaError_t launch_typed(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
                          cudaStream_t s) {
   using S = FewShape<D>;
   CUtensorMap mk, mv;
   if (!encode_pools(&mk, &mv, a, pl.hkv, D)) return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<attend_few_kernel<D>>(S::kSmem);
+  const cudaError_t e = allow_smem<attend_few_kernel<D, N>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_few_kernel<D>, dim3(tb.n_items), kFewThreads, S::kSmem, s, false, tb,
+  return launch_kernel(attend_few_kernel<D, N>, dim3(tb.n_items), kFewThreads, S::kSmem, s, false, tb,
                        static_cast<const __nv_bfloat16*>(a.q), a.q_stride, mk, mv, a.kp, a.vp, ao,
                        kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
 }
 
 }  // namespace
 
-cudaError_t launch_attend_few(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
-                              const AttendOut& ao, cudaStream_t s) {
+template <int N>
+cudaError_t launch_attend_few(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a,
+                             const AttendOut& ao, cudaStream_t s) {
   return pl.D == 128 ? launch_typed<128>(tb, pl, a, ao, s) : launch_typed<64>(tb, pl, a, ao, s);
 }
+template cudaError_t launch_attend_few(const AttendTable<kFewSeqs>&, const AttendPlan&, const AttendArgs&,
+                                      const AttendOut&, cudaStream_t);
+template cudaError_t launch_attend_few(const AttendTable<kMaxBatch>&, const AttendPlan&, const AttendArgs&,
+                                      const AttendOut&, cudaStream_t);
 
 }  // namespace wi

@@ -120,9 +120,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r != 0;
 }
-template <int D>
+
+template <int D, int N>
 __global__ void __launch_bounds__(kUThreads, 1)
-attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant__ CUtensorMap map_q,
+attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const Pool kp, const Pool vp, const AttendOut ao, float scale, uint32_t* status) {
   using S = UmmaShape<D>;
@@ -170,144 +171,144 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   const int fix_from = max(0, (first_pos + 1) / kRows - it.t0);
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 8) {
-    // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      mbar_arrive_expect(&s_q, (uint32_t)nq * S::kTile);
-      for (int i = 0; i < nq; ++i)
-        for (int c = 0; c < S::kBlocks; ++c)
-          tensor_load_3d(sq + i * S::kTile + c * S::kBlock, &map_q, 64 * c, it.h * G,
-                         it.q0 + ((it.row0 + i * kRows) >> tb.g_shift), &s_q);
-    }
-    load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
-  } else if (warp == 9) {
-    // ----------------------------------------------------------------- MMAs
-    // The whole warp runs the loop, so that addresses and descriptors stay in
-    // uniform registers; one elected lane issues each batch.
-    constexpr uint32_t kIdescS = umma_idesc_bf16_f32<128, 128>();
-    constexpr uint32_t kIdescO = umma_idesc_bf16_f32<128, D>() | kIdescBMn;
-    constexpr uint64_t kStep = S::kTile >> 4;   // a stage, in descriptor units
-    const uint64_t dq = umma_desc_sw128(smem_addr(sq)), dk = umma_desc_sw128(smem_addr(ring));
-    const uint64_t dv = umma_desc_sw128_mn(smem_addr(ring), S::kBlock);
-    auto scores = [&](int i, int st, bool last) {   // S_i = Q_i K^T
-      if (elect_one()) {
-        const uint64_t a = dq + i * kStep, b = dk + st * kStep;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ---------------------------------------------------------------- loads
+      if (lane == 0) {
+        mbar_arrive_expect(&s_q, (uint32_t)nq * S::kTile);
+        for (int i = 0; i < nq; ++i)
+          for (int c = 0; c < S::kBlocks; ++c)
+            tensor_load_3d(sq + i * S::kTile + c * S::kBlock, &map_q, 64 * c, it.h * G,
+                           it.q0 + ((it.row0 + i * kRows) >> tb.g_shift), &s_q);
+      }
+      load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
+    } else if (warp == 9) {
+      // ----------------------------------------------------------------- MMAs
+      // The whole warp runs the loop, so that addresses and descriptors stay in
+      // uniform registers; one elected lane issues each batch.
+      constexpr uint32_t kIdescS = umma_idesc_bf16_f32<128, 128>();
+      constexpr uint32_t kIdescO = umma_idesc_bf16_f32<128, D>() | kIdescBMn;
+      constexpr uint64_t kStep = S::kTile >> 4;   // a stage, in descriptor units
+      const uint64_t dq = umma_desc_sw128(smem_addr(sq)), dk = umma_desc_sw128(smem_addr(ring));
+      const uint64_t dv = umma_desc_sw128_mn(smem_addr(ring), S::kBlock);
+      auto scores = [&](int i, int st, bool last) {   // S_i = Q_i K^T
+        if (elect_one()) {
+          const uint64_t a = dq + i * kStep, b = dk + st * kStep;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t ko = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u) >> 4;
-          umma_bf16(tmem + S::kS + i * 128, a + ko, b + ko, kIdescS, k != 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t ko = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32u) >> 4;
+            umma_bf16(tmem + S::kS + i * 128, a + ko, b + ko, kIdescS, k != 0);
+          }
+          umma_commit(&s_s[i]);
+          if (last) umma_commit(&s_empty[st]);
         }
-        umma_commit(&s_s[i]);
-        if (last) umma_commit(&s_empty[st]);
-      }
-      __syncwarp();
-    };
-    auto output = [&](int i, int st, int half, bool first) {   // O_i += P_i V, half of the keys
-      if (elect_one()) {
-        const uint64_t b = dv + st * kStep;
-#pragma unroll
-        for (int kk = 0; kk < kRows / 32; ++kk) {
-          const int k = half * (kRows / 32) + kk;
-          umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
-                       !first || kk != 0);
-        }
-        if (half == 1) {
-          umma_commit(&s_o[i]);
-          if (i == nq - 1) umma_commit(&s_empty[st]);
-        }
-      }
-      __syncwarp();
-    };
-    // a ring position: unit u in stage st, phase ph
-    auto full = [&](int st, uint32_t ph) { return wait_bar(&s_full[st], ph, status); };
-    bool ok = wait_bar(&s_q, 0, status) && full(0, 0);
-    tc_fence_after();
-    if (ok)
-      for (int i = 0; i < nq; ++i) scores(i, 0, i == nq - 1);
-    if (fix_from == 0 && lane == 0) mbar_arrive(&s_go[0]);
-    int st = 1;
-    uint32_t ph = 0;
-    for (int j = 0; j < n && ok; ++j) {
-      // the diagonal's values are looked at a tile ahead of their product
-      if (j + 1 >= fix_from && j + 1 < n && lane == 0) mbar_arrive(&s_go[(j + 1) & 1]);
-      const bool fix = j >= fix_from;
-      if (!(ok = full(st, ph))) break;   // V_j
-      const int sv = st;
-      if (++st == S::kStages) { st = 0; ph ^= 1; }
-      for (int i = 0; i < nq && ok; ++i) {
-        ok = wait_bar(&s_p[i][0], (uint32_t)j & 1u, status);
-        if (ok && fix && i == 0) ok = wait_bar(&s_fixed[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
-        if (!ok) break;
-        tc_fence_after();
-        output(i, sv, 0, j == 0);
-        if (!(ok = wait_bar(&s_p[i][1], (uint32_t)j & 1u, status))) break;
-        tc_fence_after();
-        output(i, sv, 1, false);
-        if (j + 1 < n) {
-          if (i == 0 && !(ok = full(st, ph))) break;   // K_(j + 1)
-          tc_fence_after();
-          scores(i, st, i == nq - 1);
-        }
-      }
-      if (++st == S::kStages) { st = 0; ph ^= 1; }
-    }
-    // every MMA issued has completed before the columns are released
-    if (elect_one()) umma_commit(&s_done);
-    __syncwarp();
-    wait_bar(&s_done, 0, status);
-  } else if (warp >= 10) {
-    // ------------------------------------------- value tiles on the diagonal
-    for (int j = fix_from; j < n; ++j) {
-      // (the ring's phase of V_j is known only from a permission in the MMA
-      // warp's order; two of them alternate, as the next may come before this
-      // one is seen)
-      const int u = 2 * j + 1, base = (it.t0 + j) * kRows;
-      bool ok = wait_bar(&s_go[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
-      ok = ok && wait_bar(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      unsigned char* tile = ring + (size_t)(u % S::kStages) * S::kTile;
-      constexpr int CH = D / 8;
-      auto chunk_at = [&](int c) {
-        return reinterpret_cast<uint4*>(tile + ((c % CH) >> 3) * S::kBlock + swz128(c / CH, c & 7));
+        __syncwarp();
       };
-      const int r0 = max(0, first_pos + 1 - base);   // the first row some query does not see
-      const int r1 = min(kRows, it.key_end - base);     // the first row none sees
-      const int at0 = 32 * (warp - 10) + lane;
-#pragma unroll 4
-      for (int c = r1 * CH + at0; c < kRows * CH; c += 64) *chunk_at(c) = make_uint4(0u, 0u, 0u, 0u);
-      // four chunks in flight; a product with 0 tells whether all eight
-      // values of a chunk are finite (0 or NaN)
-      bool bad = false;
-#pragma unroll 1
-      for (int c0 = r0 * CH + at0; c0 < r1 * CH; c0 += 256) {
-        uint4 x[4];
+      auto output = [&](int i, int st, int half, bool first) {   // O_i += P_i V, half of the keys
+        if (elect_one()) {
+          const uint64_t b = dv + st * kStep;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = *chunk_at(min(c0 + 64 * e, r1 * CH - 1));
-        uint32_t odd = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) odd |= nonfinite(x[e]) ? 1u << e : 0u;
-        if (odd == 0) continue;
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          if (!((odd >> e) & 1u) || c0 + 64 * e >= r1 * CH) continue;
-          uint32_t* w = reinterpret_cast<uint32_t*>(chunk_at(c0 + 64 * e));
-          bad = true;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v = w[q];
-            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
-            w[q] = v;
+          for (int kk = 0; kk < kRows / 32; ++kk) {
+            const int k = half * (kRows / 32) + kk;
+            umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
+                         !first || kk != 0);
+          }
+          if (half == 1) {
+            umma_commit(&s_o[i]);
+            if (i == nq - 1) umma_commit(&s_empty[st]);
           }
         }
+        __syncwarp();
+      };
+      // a ring position: unit u in stage st, phase ph
+      auto full = [&](int st, uint32_t ph) { return wait_bar(&s_full[st], ph, status); };
+      bool ok = wait_bar(&s_q, 0, status) && full(0, 0);
+      tc_fence_after();
+      if (ok)
+        for (int i = 0; i < nq; ++i) scores(i, 0, i == nq - 1);
+      if (fix_from == 0 && lane == 0) mbar_arrive(&s_go[0]);
+      int st = 1;
+      uint32_t ph = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        // the diagonal's values are looked at a tile ahead of their product
+        if (j + 1 >= fix_from && j + 1 < n && lane == 0) mbar_arrive(&s_go[(j + 1) & 1]);
+        const bool fix = j >= fix_from;
+        if (!(ok = full(st, ph))) break;   // V_j
+        const int sv = st;
+        if (++st == S::kStages) { st = 0; ph ^= 1; }
+        for (int i = 0; i < nq && ok; ++i) {
+          ok = wait_bar(&s_p[i][0], (uint32_t)j & 1u, status);
+          if (ok && fix && i == 0) ok = wait_bar(&s_fixed[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
+          if (!ok) break;
+          tc_fence_after();
+          output(i, sv, 0, j == 0);
+          if (!(ok = wait_bar(&s_p[i][1], (uint32_t)j & 1u, status))) break;
+          tc_fence_after();
+          output(i, sv, 1, false);
+          if (j + 1 < n) {
+            if (i == 0 && !(ok = full(st, ph))) break;   // K_(j + 1)
+            tc_fence_after();
+            scores(i, st, i == nq - 1);
+          }
+        }
+        if (++st == S::kStages) { st = 0; ph ^= 1; }
       }
-      if (bad) atomicOr(&s_bad, 1u);
-      fence_proxy_async();
+      // every MMA issued has completed before the columns are released
+      if (elect_one()) umma_commit(&s_done);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_fixed[j & 1]);
+      wait_bar(&s_done, 0, status);
+    } else if (warp >= 10) {
+      // ------------------------------------------- value tiles on the diagonal
+      for (int j = fix_from; j < n; ++j) {
+        // (the ring's phase of V_j is known only from a permission in the MMA
+        // warp's order; two of them alternate, as the next may come before this
+        // one is seen)
+        const int u = 2 * j + 1, base = (it.t0 + j) * kRows;
+        bool ok = wait_bar(&s_go[j & 1], (uint32_t)((j - fix_from) >> 1) & 1u, status);
+        ok = ok && wait_bar(&s_full[u % S::kStages], (uint32_t)(u / S::kStages) & 1u, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        unsigned char* tile = ring + (size_t)(u % S::kStages) * S::kTile;
+        constexpr int CH = D / 8;
+        auto chunk_at = [&](int c) {
+          return reinterpret_cast<uint4*>(tile + ((c % CH) >> 3) * S::kBlock + swz128(c / CH, c & 7));
+        };
+        const int r0 = max(0, first_pos + 1 - base);   // the first row some query does not see
+        const int r1 = min(kRows, it.key_end - base);   // the first row none sees
+        const int at0 = 32 * (warp - 10) + lane;
+#pragma unroll 4
+        for (int c = r1 * CH + at0; c < kRows * CH; c += 64) *chunk_at(c) = make_uint4(0u, 0u, 0u, 0u);
+        // four chunks in flight; a product with 0 tells whether all eight
+        // values of a chunk are finite (0 or NaN)
+        bool bad = false;
+#pragma unroll 1
+        for (int c0 = r0 * CH + at0; c0 < r1 * CH; c0 += 256) {
+          uint4 x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = *chunk_at(min(c0 + 64 * e, r1 * CH - 1));
+          uint32_t odd = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= nonfinite(x[e]) ? 1u << e : 0u;
+          if (odd == 0) continue;
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            if (!((odd >> e) & 1u) || c0 + 64 * e >= r1 * CH) continue;
+            uint32_t* w = reinterpret_cast<uint32_t*>(chunk_at(c0 + 64 * e));
+            bad = true;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v = w[q];
+              if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+              if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+              w[q] = v;
+            }
+          }
+        }
+        if (bad) atomicOr(&s_bad, 1u);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_fixed[j & 1]);
+      }
     }
-  }
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -478,8 +479,8 @@ attend_umma_kernel(const __grid_constant__ AttendTable tb, const __grid_constant
   }
 }
 
-template <int D>
-cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
+template <int D, int N>
+cudaError_t launch_typed(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
                          cudaStream_t s) {
   using S = UmmaShape<D>;
   CUtensorMap mq, mk, mv;
@@ -489,17 +490,22 @@ cudaError_t launch_typed(const AttendTable& tb, const AttendPlan& pl, const Atte
   const cuuint32_t qb[3] = {64, (cuuint32_t)pl.G, (cuuint32_t)(kRows / pl.G)};
   if (!encode_map(&mq, 3, a.q, qd, qs, qb) || !encode_pools(&mk, &mv, a, pl.hkv, D))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<attend_umma_kernel<D>>(S::kSmem);
+  const cudaError_t e = allow_smem<attend_umma_kernel<D, N>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_umma_kernel<D>, dim3(tb.n_items), kUThreads, S::kSmem, s, false, tb, mq, mk, mv, a.kp,
+  return launch_kernel(attend_umma_kernel<D, N>, dim3(tb.n_items), kUThreads, S::kSmem, s, false, tb, mq, mk, mv, a.kp,
                        a.vp, ao, kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
 }
 
 }  // namespace
 
-cudaError_t launch_attend_umma(const AttendTable& tb, const AttendPlan& pl, const AttendArgs& a,
-                               const AttendOut& ao, cudaStream_t s) {
+template <int N>
+cudaError_t launch_attend_umma(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a,
+                             const AttendOut& ao, cudaStream_t s) {
   return pl.D == 128 ? launch_typed<128>(tb, pl, a, ao, s) : launch_typed<64>(tb, pl, a, ao, s);
 }
+template cudaError_t launch_attend_umma(const AttendTable<kFewSeqs>&, const AttendPlan&, const AttendArgs&,
+                                      const AttendOut&, cudaStream_t);
+template cudaError_t launch_attend_umma(const AttendTable<kMaxBatch>&, const AttendPlan&, const AttendArgs&,
+                                      const AttendOut&, cudaStream_t);
 
 }  // namespace wi

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const AppendA
 // Key runs per block (ns).  Many blocks: one run each, and the item grid
 // fills the SMs.  Few: the key axis is split until the longest item and the
 // work per SM balance, in key tiles (attend_shape has the other costs).
-constexpr double kMergeCost = 2.0;   // the merge's launch
+constexpr double kMergeCost = 3.0;   // the merge's launch and latency (about 4 us)
 constexpr int kMinTiles = 2, kMaxSplit = 148;
 
 int64_t tiles_of(const AttendSeq& s, int G, int R, int KT, int blk) {
