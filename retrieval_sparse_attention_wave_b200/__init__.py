@@ -766,7 +766,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
 
 @dataclass
 class AttendParams:
-    """q_lens[b]: query tokens of sequence b, its last ones (None: all of them)."""
+    """q_lens[b]: query tokens of sequence b, its last ones (None: all of them).
+    The list is read when the object is made."""
     n_q_heads: int
     q_lens: Optional[List[int]] = None
 

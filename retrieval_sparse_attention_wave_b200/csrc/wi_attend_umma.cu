@@ -5,6 +5,9 @@
 // memory):
 //   S_i = Q_i K_j^T;   P_i = 2^(c S_i - m_i) as bf16, over S_i's columns;
 //   O_i += P_i V_j     (P_i straight from tensor memory).
+// The weights are rounded to bf16, the type of the values they multiply (half
+// a step, 2^-8 of a weight, averages out over the keys; the output's own
+// rounding is as large); their sum is taken before that, in fp32.
 // Roles:
 //   warps 0..3, 4..7  softmax of query tile 0, 1: a thread owns a row
 //                     (a tensor-memory lane), so its maximum, mass and output
