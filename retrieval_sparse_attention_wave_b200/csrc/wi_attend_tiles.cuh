@@ -47,6 +47,12 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
+// A 16-byte asynchronous copy, or 16 bytes of zeros with nothing read.
+__device__ __forceinline__ void cp_async16_or_zero(void* smem, const void* gmem, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(gmem), "r"(copy ? 16 : 0)
+               : "memory");
+}
+
 // One warp loads an item's key and value tiles in the order K_0, V_0, K_1, V_1,
 // ... (unit u into stage u % kStages): a tensor copy per page and 64 channels.
 template <int D, int kStages>
@@ -97,32 +103,58 @@ __device__ __forceinline__ void load_units(const Item& it, int hkv, const Pool& 
         wait_bar(&s_full[u % kStages], (uint32_t)(u / kStages) & 1u, status);
   } else {
     // pages of fewer than 8 rows: 16-byte copies into the swizzled layout,
-    // two units behind the one being issued
+    // arriving two units behind the one being issued.  Lane l looks up rows l,
+    // l + 32, l + 64 and l + 96 of a tile, a tile ahead; the copies of a row
+    // get its place by a shuffle.  One warp's issue bounds it: 8192 tokens on
+    // pages of one take 750 us, of 16 (tensor copies) 442.
     constexpr int CH = D / 8, kLag = 2;
     auto arrive = [&](int u) {
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_full[u % kStages]);
     };
-    int u = 0;
-    for (; u < 2 * n && ok; ++u) {
-      const int t = it.t0 + u / 2, st = u % kStages;
-      if (u >= kStages) ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / kStages - 1) & 1u, status));
-      if (!ok) break;
-      const Pool& p = u & 1 ? vp : kp;
-      unsigned char* dst = ring + (size_t)st * kTile;
-#pragma unroll 4
-      for (int i = lane; i < kRows * CH; i += 32) {
-        const int r = i / CH, ch = i % CH, key = t * kRows + r;
-        const int64_t row = key < it.key_end ? pool_row(p, hkv, D, it.b, it.h, key, status) : -1;
-        unsigned char* to = dst + (ch >> 3) * kBlock + swz128(r, ch & 7);
-        if (row >= 0) cp_async16(to, reinterpret_cast<const __nv_bfloat16*>(p.base) + row + ch * 8);
-        else *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
+    auto key_of = [&](int j, int i) { return (it.t0 + j) * kRows + 32 * i + lane; };
+    auto page_at = [&](int j, int i) {
+      return j < n && key_of(j, i) < it.key_end ? __ldg(bt + (key_of(j, i) >> kp.page_shift)) : -1;
+    };
+    int page[4], u = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) page[i] = page_at(0, i);
+    for (int j = 0; j < n && ok; ++j) {
+      int y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = key_of(j, i);
+        y[i] = -1;
+        if (key < it.key_end) {
+          if (page[i] >= 0 && page[i] < kp.n_pages)
+            y[i] = ((page[i] * hkv + it.h) << kp.page_shift) + (key & page_mask);
+          else
+            flag_error(status, WI_DEV_BAD_PAGE);
+        }
+        page[i] = page_at(j + 1, i);
       }
-      cp_async_commit();
-      if (u >= kLag) {
-        cp_async_wait<kLag>();
-        arrive(u - kLag);
+      for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+        const int st = u % kStages;
+        if (u >= kStages)
+          ok = __all_sync(0xffffffffu, wait_bar(&s_empty[st], (uint32_t)(u / kStages - 1) & 1u, status));
+        if (!ok) break;
+        const int ch = lane % CH;
+        const __nv_bfloat16* base = reinterpret_cast<const __nv_bfloat16*>(kv ? vp.base : kp.base) + ch * 8;
+        unsigned char* dst = ring + (size_t)st * kTile + (ch >> 3) * kBlock;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll 4
+          for (int k = 0; k < CH; ++k) {
+            const int r = k * (32 / CH) + lane / CH;
+            const int row = __shfl_sync(0xffffffffu, y[i], r);
+            cp_async16_or_zero(dst + swz128(32 * i + r, ch & 7), base + (int64_t)max(row, 0) * D, row >= 0);
+          }
+        cp_async_commit();
+        if (u >= kLag) {
+          cp_async_wait<kLag>();
+          arrive(u - kLag);
+        }
       }
     }
     cp_async_wait<0>();
