@@ -775,11 +775,13 @@ class AttendParams:
         self._q_lens = None if self.q_lens is None else _i32_array(self.q_lens)
         self._q_ptr = (None if self.q_lens is None
                        else C.cast(self._q_lens, C.POINTER(C.c_int32)))
+        self._total = None if self.q_lens is None else sum(self._q_lens)
 
     def n_queries(self, kv: KVCache) -> int:
-        _need(self._q_lens is None or len(self._q_lens) == len(kv.seq_lens),
-              "q_lens: one entry per sequence is expected")
-        return sum(kv.seq_lens if self._q_lens is None else self._q_lens)
+        if self._q_lens is None:
+            return sum(kv.seq_lens)
+        _need(len(self._q_lens) == len(kv.seq_lens), "q_lens: one entry per sequence is expected")
+        return self._total
 
     def c_struct(self, q_stride: int = 0, out_stride: int = 0) -> WiAttendParams:
         return WiAttendParams(self.n_q_heads, self._q_ptr, q_stride, out_stride)

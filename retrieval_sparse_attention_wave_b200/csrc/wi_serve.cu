@@ -247,11 +247,11 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   const int R = sh.rows, KT = sh.keys, slots = sh.slots;
   double total = 0;
   int64_t longest = 0;
-  int32_t most[kMaxBatch], least[kMaxBatch];   // tiles of a sequence's last and first block
+  uint32_t most[kMaxBatch], least[kMaxBatch];   // tiles of a sequence's last and first block
   for (int i = 0; i < pl.n_seq; ++i) {
     AttendSeq& s = pl.seq[i];
-    most[i] = (int32_t)tiles_of(s, pl.G, R, KT, s.nblk - 1);
-    least[i] = (int32_t)tiles_of(s, pl.G, R, KT, 0);
+    most[i] = (uint32_t)tiles_of(s, pl.G, R, KT, s.nblk - 1);
+    least[i] = (uint32_t)tiles_of(s, pl.G, R, KT, 0);
     total += 0.5 * ((double)most[i] + least[i]) * s.nblk * pl.hkv;
     longest = std::max<int64_t>(longest, most[i]);
     s.ns = 1;
@@ -262,7 +262,8 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
     double items = 0, parts = 0;   // parts in full blocks
     for (int i = 0; i < pl.n_seq; ++i) {
       const AttendSeq& s = pl.seq[i];
-      const double runs = 0.5 * (double)(cdiv(most[i], C) + cdiv(least[i], C));
+      const uint32_t c = (uint32_t)C;
+      const double runs = 0.5 * (double)((most[i] + c - 1) / c + (least[i] + c - 1) / c);
       items += s.nblk * pl.hkv * runs;
       if (runs > 1) parts += pl.hkv * runs * std::min<double>((double)s.n * pl.G / R, s.nblk);
     }
@@ -272,8 +273,10 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   };
   int64_t best = longest;
   double cheapest = cost(longest);
-  // (fewer candidates with many sequences: 17 for 256 of them)
-  for (int k = 2; k <= kMaxSplit; k += 1 + k * pl.n_seq / 1024) {
+  // (a candidate costs two divisions a sequence: all 147 for up to two
+  // sequences, 29 or 17 of them for more)
+  const int coarse = pl.n_seq <= 2 ? kMaxSplit + 1 : pl.n_seq <= 32 ? 8 : 4;
+  for (int k = 2; k <= kMaxSplit; k += 1 + k / coarse) {
     const int64_t C = cdiv(longest, k);
     if (C < kMinTiles) break;
     const double c = cost(C);
