@@ -52,7 +52,7 @@ int esize(wi_dtype d) { return d == WI_BF16 ? 2 : 4; }
 // Common geometry checks for a paged pool description.
 wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int64_t n_pages,
                        const void* kp, const void* vp, const int32_t* bt, int max_pages,
-                       const int32_t* seq_lens) {
+                       const int32_t* seq_lens, int min_len) {
   if (dtype != WI_F32 && dtype != WI_BF16) return WI_ERR_INVALID_ARG;
   if (batch < 1 || hkv < 1 || d < 1 || page < 1 || n_pages < 1 || max_pages < 1)
     return WI_ERR_INVALID_ARG;
@@ -64,7 +64,7 @@ wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int6
   int64_t tot = 0;
   for (int b = 0; b < batch; ++b) {
     const int64_t T = seq_lens[b];
-    if (T < 1) return WI_ERR_INVALID_ARG;
+    if (T < min_len) return WI_ERR_INVALID_ARG;
     if (cdiv(T, page) > max_pages) return WI_ERR_INVALID_ARG;
     tot += T;
   }

@@ -293,7 +293,7 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
   if (!kv || !p) return WI_ERR_INVALID_ARG;
   wi_status st = check_common(kv->dtype, kv->batch, kv->n_kv_heads, kv->head_dim, kv->page_size,
                               kv->n_pages, kv->k_pool, kv->v_pool, kv->block_table, kv->max_pages,
-                              kv->seq_lens);
+                              kv->seq_lens, 0);
   if (st != WI_OK) return st;
   const int H = kv->n_kv_heads;
   if (p->n_q_heads < 1 || p->n_q_heads % H != 0) return WI_ERR_INVALID_ARG;

@@ -13,7 +13,7 @@ namespace wi {
 wi_status cuda_fail(cudaError_t e);
 wi_status check_common(wi_dtype dtype, int batch, int hkv, int d, int page, int64_t n_pages,
                        const void* kp, const void* vp, const int32_t* bt, int max_pages,
-                       const int32_t* seq_lens);
+                       const int32_t* seq_lens, int min_len = 1);
 
 // A launch whose error is its own (cudaGetLastError after <<<>>> would also
 // hand back what an earlier call of this thread left).

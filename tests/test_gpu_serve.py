@@ -230,7 +230,8 @@ def test_attend_page_sizes(dtype, page):
 @pytest.mark.parametrize("lens,q_lens", [
     ([1], [1]), ([128], [1]), ([129], [1]), ([5000], [1]), ([3000, 1, 777], [1, 1, 1]),
     ([2500], [3]), ([2500, 900], [33, 900]), ([1025, 1024, 1023], [65, 64, 63]),
-    ([600, 600, 600], [0, 600, 0]), ([4000, 200], [0, 1]),
+    ([600, 600, 600], [0, 600, 0]), ([4000, 200], [0, 1]), ([0, 70, 0], [0, 70, 0]),
+    ([0, 1700, 0, 3], [0, 1, 0, 1]),
 ])
 @pytest.mark.parametrize("H,G,d", [(1, 8, 128), (2, 1, 64), (4, 4, 128)])
 def test_attend_chunks_and_single_tokens(dtype, lens, q_lens, H, G, d):

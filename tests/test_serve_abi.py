@@ -117,7 +117,9 @@ def attend_size(kv, p):
     (dict(), dict(q_stride=4095), W.WI_ERR_INVALID_ARG),
     (dict(), dict(out_stride=4100), W.WI_ERR_INVALID_ARG),
     (dict(), dict(q_stride=6144), W.WI_OK),
-    (dict(seq=[0]), dict(), W.WI_ERR_INVALID_ARG),
+    (dict(seq=[0]), dict(), W.WI_OK),                        # an empty slot of a batch
+    (dict(seq=[0]), dict(q_lens=[1]), W.WI_ERR_INVALID_ARG),
+    (dict(seq=[-1]), dict(), W.WI_ERR_INVALID_ARG),
     (dict(seq=[70000]), dict(), W.WI_ERR_INVALID_ARG),       # more pages than the table's row
     (dict(head_dim=96), dict(), W.WI_ERR_UNSUPPORTED),
     (dict(n_pages=2 ** 25), dict(), W.WI_ERR_UNSUPPORTED),   # pool rows pass 32 bits
