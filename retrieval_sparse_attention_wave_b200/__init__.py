@@ -242,7 +242,12 @@ class KVCache:
     seq_lens: List[int]
 
     def __post_init__(self):
-        self._seq = _i32_array(self.seq_lens)
+        self._read_lens()
+
+    def _read_lens(self):
+        lens = tuple(self.seq_lens)
+        if lens != getattr(self, "_lens", None):   # the list may change between calls
+            self._seq, self._lens = _i32_array(lens), lens
 
     @property
     def n_kv_heads(self) -> int:
@@ -257,12 +262,7 @@ class KVCache:
         return self.k_pool.shape[3]
 
     def c_struct(self) -> WiKVCache:
-        # kept while the buffers it points at are the same (a step per layer
-        # marshals the same cache)
-        sig = (self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.block_table.data_ptr(),
-               self.k_pool.shape, self.k_pool.dtype, self.block_table.shape, id(self._seq))
-        if getattr(self, "_cs_sig", None) == sig:
-            return self._cs
+        self._read_lens()
         s = WiKVCache()
         s.dtype = _dtype_code(self.k_pool.dtype)
         s.batch = len(self.seq_lens)
@@ -275,8 +275,17 @@ class KVCache:
         s.block_table = self.block_table.data_ptr()
         s.max_pages = self.block_table.shape[1]
         s.seq_lens = C.cast(self._seq, C.POINTER(C.c_int32))
-        self._cs, self._cs_sig = s, sig
         return s
+
+    def _struct(self) -> WiKVCache:
+        """c_struct(), kept while what it says is the same (a step marshals the
+        same cache for every layer's call).  For reading only."""
+        self._read_lens()
+        sig = (self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.block_table.data_ptr(),
+               self.k_pool.shape, self.k_pool.dtype, self.block_table.shape, self._lens)
+        if getattr(self, "_cs_sig", None) != sig:
+            self._cs, self._cs_sig = self.c_struct(), sig
+        return self._cs
 
 
 # ---------------------------------------------------------------- the index
@@ -790,7 +799,7 @@ class AttendParams:
 def attend_workspace_bytes(kv: KVCache, params: AttendParams) -> int:
     params.n_queries(kv)
     n = C.c_size_t()
-    s, p = kv.c_struct(), params.c_struct()
+    s, p = kv._struct(), params.c_struct()
     _check(_lib.wi_attend_workspace_size(C.byref(s), C.byref(p), C.byref(n)),
            "wi_attend_workspace_size")
     return n.value
@@ -838,7 +847,7 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     if ws is None:
         ws = attend_workspace(kv, params)
     _on_gpu("ws", ws, torch.uint8, dev)
-    c, p = kv.c_struct(), params.c_struct(qs, os_)
+    c, p = kv._struct(), params.c_struct(qs, os_)
     _check(_lib.wi_attend(q.data_ptr(), C.byref(c), C.byref(p), out.data_ptr(), lse.data_ptr(),
                           ws.data_ptr(), ws.numel(), _current_stream(dev)),
            "wi_attend")

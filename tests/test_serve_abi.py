@@ -181,6 +181,24 @@ def test_python_checks_name_the_argument():
         W.plan_pages(table, torch.ones(2, dtype=torch.int32), 8)
 
 
+def test_cache_lengths_may_change_between_calls():
+    kv = W.KVCache(torch.zeros(4, 2, 16, 64), torch.zeros(4, 2, 16, 64),
+                   torch.zeros(2, 4, dtype=torch.int32), [40, 3])
+    prm = W.AttendParams(4)
+    one = kv.c_struct()
+    assert prm.n_queries(kv) == 43 and kv._struct() is kv._struct()
+    kv.seq_lens[1] += 1
+    assert prm.n_queries(kv) == 44
+    assert [kv._struct().seq_lens[b] for b in range(2)] == [40, 4]
+    assert [kv.c_struct().seq_lens[b] for b in range(2)] == [40, 4]
+    kv.seq_lens.pop()
+    assert kv._struct().batch == kv.c_struct().batch == 1 and prm.n_queries(kv) == 40
+    assert one.batch == 2 and [one.seq_lens[b] for b in range(2)] == [40, 3]
+    mine = kv.c_struct()      # a caller's own: changing it changes no later call
+    mine.batch = 7
+    assert kv._struct().batch == 1
+
+
 def test_plain_plan_by_hand():
     # page 4; request 0 has 5 tokens (pages 9, 3) and gets 4: one new page;
     # request 1 is new and gets 5: two pages; the stack's end goes first
