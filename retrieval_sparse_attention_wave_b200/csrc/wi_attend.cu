@@ -239,19 +239,19 @@ attend_fma_kernel(const __grid_constant__ AttendTable<N> tb, const float* __rest
 
 // ------------------------------------------------------------------ merge
 // The parts' (m, l) of a query row of a split sequence give the weights
-// 2^(m_s - m); the parts' outputs are added in order.  A warp per row, or,
-// where the rows are few (single tokens), a CTA per row whose four warps take
-// every fourth part and add up in a fixed order.
+// 2^(m_s - m); the parts' outputs are added in order.
 constexpr int kMergeWarps = 4;
+constexpr int kMergeLanes = 8;   // of a row, where rows are many
+constexpr int kMergeRows = 32 * kMergeWarps / kMergeLanes;
 
-template <typename T, int D, bool kWide, int N>
-__global__ void __launch_bounds__(32 * kMergeWarps)
-attend_merge_kernel(const __grid_constant__ AttendTable<N> tb, int n_rows, const AttendOut ao) {
-  constexpr int E = D / 32;   // columns per lane
-  constexpr int kStep = kWide ? kMergeWarps : 1;
-  __shared__ float s_o[kWide ? kMergeWarps : 1][D], s_l[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
-  const int x = kWide ? (int)blockIdx.x : (int)blockIdx.x * kMergeWarps + warp;
+struct MergeRow {
+  int64_t part, tok;   // its first part (the next one Rb rows on), its token
+  uint32_t Rb;
+  int ns, head;
+};
+
+template <int N>
+__device__ inline MergeRow merge_row(const AttendTable<N>& tb, int x) {
   int lo = 0, hi = tb.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -261,34 +261,114 @@ attend_merge_kernel(const __grid_constant__ AttendTable<N> tb, int n_rows, const
   const uint32_t all = (uint32_t)s.n << tb.g_shift, Rb = min((uint32_t)tb.rows, all);
   const uint32_t in = (uint32_t)(x - s.mrow0), h = in / all, row = in - h * all;
   const uint32_t blk = row / (uint32_t)tb.rows, rr = row - blk * tb.rows;
-  const int64_t part = s.part0 + ((int64_t)blk * tb.hkv + h) * s.ns * Rb + rr;
   // its block's runs
   const uint32_t last = min((blk + 1) * (uint32_t)tb.rows, all) - 1;
   const uint32_t tiles = ((uint32_t)(s.T - s.n) + (last >> tb.g_shift) + tb.keys) / tb.keys;   // (of the keys its last row sees)
-  const int ns = (int)((tiles + s.run - 1) / s.run);
+  MergeRow r;
+  r.part = s.part0 + ((int64_t)blk * tb.hkv + h) * s.ns * Rb + rr;
+  r.tok = s.q0 + (row >> tb.g_shift);
+  r.Rb = Rb;
+  r.ns = (int)((tiles + s.run - 1) / s.run);
+  r.head = (int)(h << tb.g_shift) + (int)(row & ((1u << tb.g_shift) - 1));
+  return r;
+}
+
+__device__ inline void store4(float* to, float4 f) { *reinterpret_cast<float4*>(to) = f; }
+__device__ inline void store4(__nv_bfloat16* to, float4 f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
+  *reinterpret_cast<uint2*>(to) = make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
+}
+
+// Many rows: eight lanes a row, so that a warp has four rows' loads in flight
+// and looks up four rows at once.
+template <typename T, int D, int N>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+attend_merge_rows_kernel(const __grid_constant__ AttendTable<N> tb, int n_rows, const AttendOut ao) {
+  constexpr int C = D / (4 * kMergeLanes);   // quads of columns per lane
+  const int sub = threadIdx.x & (kMergeLanes - 1);
+  const int x = (int)blockIdx.x * kMergeRows + (int)threadIdx.x / kMergeLanes;
+  MergeRow r = merge_row(tb, min(x, n_rows - 1));
+  if (x >= n_rows) r.ns = 0;   // (its lanes stay for the shuffles)
+  const int ns_warp = (int)__reduce_max_sync(0xffffffffu, (unsigned)r.ns);
   pdl_wait();   // the parts are there
+  const float2* ml = ao.ml + r.part;
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 mine = sub < r.ns ? __ldcg(ml + (int64_t)sub * r.Rb) : none;
+  float m = mine.x;
+  for (int i = sub + kMergeLanes; i < r.ns; i += kMergeLanes)
+    m = fmaxf(m, __ldcg(ml + (int64_t)i * r.Rb).x);
+#pragma unroll
+  for (int k = 1; k < kMergeLanes; k *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < ns_warp; i0 += kMergeLanes) {
+    const int at = i0 + sub;
+    const float2 f = i0 == 0 ? mine : at < r.ns ? __ldcg(ml + (int64_t)at * r.Rb) : none;
+    const float w = at < r.ns ? exp2f(f.x - mu) : 0.f;
+    l = fmaf(w, f.y, l);
+    const int n = min(kMergeLanes, ns_warp - i0);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i, kMergeLanes);
+      if (i0 + i < r.ns) {
+        const float4* from = reinterpret_cast<const float4*>(ao.o + (r.part + (int64_t)(i0 + i) * r.Rb) * D) + sub;
+        float4 v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = __ldcg(from + kMergeLanes * c);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          o[c].x = fmaf(wi, v[c].x, o[c].x);
+          o[c].y = fmaf(wi, v[c].y, o[c].y);
+          o[c].z = fmaf(wi, v[c].z, o[c].z);
+          o[c].w = fmaf(wi, v[c].w, o[c].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 1; k < kMergeLanes; k *= 2) l += __shfl_xor_sync(0xffffffffu, l, k);
   if (x >= n_rows) return;
+  if (sub == 0 && ao.lse) ao.lse[r.tok * ao.Hq + r.head] = kLn2 * (m + log2f(l));
+  const float inv = 1.f / l;
+  T* to = reinterpret_cast<T*>(ao.out) + r.tok * ao.stride + (int64_t)r.head * D + 4 * sub;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    store4(to + 4 * kMergeLanes * c, make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv));
+}
+
+// Few rows (single tokens): a CTA per row, whose four warps take every fourth
+// part and add up in a fixed order.
+template <typename T, int D, int N>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+attend_merge_kernel(const __grid_constant__ AttendTable<N> tb, const AttendOut ao) {
+  constexpr int E = D / 32;   // columns per lane
+  __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  const MergeRow r = merge_row(tb, (int)blockIdx.x);
+  pdl_wait();   // the parts are there
   float m = -INFINITY;
-  for (int i = lane; i < ns; i += 32) m = fmaxf(m, __ldcg(&ao.ml[part + (int64_t)i * Rb]).x);
+  for (int i = lane; i < r.ns; i += 32) m = fmaxf(m, __ldcg(&ao.ml[r.part + (int64_t)i * r.Rb]).x);
   m = warp_max(m);
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  // parts first, first + kStep, ..., 32 of them at a time
-  const int first = kWide ? warp : 0;
-  for (int i0 = first; i0 < ns; i0 += 32 * kStep) {
+  // parts warp, warp + kMergeWarps, ..., 32 of them at a time
+  for (int i0 = warp; i0 < r.ns; i0 += 32 * kMergeWarps) {
     float w = 0.f;
-    if (i0 + kStep * lane < ns) {
-      const float2 ml = __ldcg(&ao.ml[part + (int64_t)(i0 + kStep * lane) * Rb]);
+    if (i0 + kMergeWarps * lane < r.ns) {
+      const float2 ml = __ldcg(&ao.ml[r.part + (int64_t)(i0 + kMergeWarps * lane) * r.Rb]);
       w = exp2f(ml.x - mu);
       l = fmaf(w, ml.y, l);
     }
-    const int n = min(32, (ns - i0 + kStep - 1) / kStep);
+    const int n = min(32, (r.ns - i0 + kMergeWarps - 1) / kMergeWarps);
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* from = ao.o + (part + (int64_t)(i0 + kStep * i) * Rb) * D + lane * E;
+      const float* from = ao.o + (r.part + (int64_t)(i0 + kMergeWarps * i) * r.Rb) * D + lane * E;
       float v[E];
       if constexpr (E == 4) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(from));
@@ -302,22 +382,18 @@ attend_merge_kernel(const __grid_constant__ AttendTable<N> tb, int n_rows, const
     }
   }
   l = warp_sum(l);
-  if constexpr (kWide) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (warp != 0) return;
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = (s_o[0][lane * E + e] + s_o[1][lane * E + e]) + (s_o[2][lane * E + e] + s_o[3][lane * E + e]);
-  }
-  const int64_t tok = s.q0 + (row >> tb.g_shift);
-  const int head = (int)(h << tb.g_shift) + (int)(row & ((1u << tb.g_shift) - 1));
-  if (lane == 0 && ao.lse) ao.lse[tok * ao.Hq + head] = kLn2 * (m + log2f(l));
+  for (int e = 0; e < E; ++e)
+    o[e] = (s_o[0][lane * E + e] + s_o[1][lane * E + e]) + (s_o[2][lane * E + e] + s_o[3][lane * E + e]);
+  if (lane == 0 && ao.lse) ao.lse[r.tok * ao.Hq + r.head] = kLn2 * (m + log2f(l));
   const float inv = 1.f / l;
-  T* to = reinterpret_cast<T*>(ao.out) + tok * ao.stride + (int64_t)head * D + lane * E;
+  T* to = reinterpret_cast<T*>(ao.out) + r.tok * ao.stride + (int64_t)r.head * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) store_elem(to + e, o[e] * inv);
 }
@@ -336,10 +412,10 @@ cudaError_t launch_fma(const AttendTable<N>& tb, const AttendArgs& a, const Atte
 
 template <typename T, int D, int N>
 cudaError_t launch_merge(const AttendTable<N>& tb, int n_rows, const AttendOut& ao, cudaStream_t s) {
-  const bool wide = n_rows <= 16 * 148;   // one wave of CTAs
-  const dim3 grid((unsigned)(wide ? n_rows : (n_rows + kMergeWarps - 1) / kMergeWarps));
-  return launch_kernel(wide ? attend_merge_kernel<T, D, true, N> : attend_merge_kernel<T, D, false, N>, grid,
-                       32 * kMergeWarps, 0, s, true, tb, n_rows, ao);
+  if (n_rows <= 16 * 148)   // one wave of CTAs
+    return launch_kernel(attend_merge_kernel<T, D, N>, dim3((unsigned)n_rows), 32 * kMergeWarps, 0, s, true, tb, ao);
+  const dim3 grid((unsigned)((n_rows + kMergeRows - 1) / kMergeRows));
+  return launch_kernel(attend_merge_rows_kernel<T, D, N>, grid, 32 * kMergeWarps, 0, s, true, tb, n_rows, ao);
 }
 
 }  // namespace
