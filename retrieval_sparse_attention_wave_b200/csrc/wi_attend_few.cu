@@ -6,12 +6,18 @@
 // tiles; warps 0..7 take 16 keys of each 128-key tile, with a running maximum,
 // mass and output of their own (products as m16n8k16: the rows are the MMA's
 // M, so the scores' accumulators are the weights' operand), and join them at
-// the end.  A tile costs a warp about 250 instructions, a third of the time
-// its 64 KB take to arrive, and a stage is free as soon as eight warps have
-// read it: the tensor-memory kernel holds its stages through a softmax of 128
-// rows, which leaves 96 KB in flight and 4.9 TB/s.  16 tokens over 32768 keys
-// each, 8 KV heads of 128: 328 us, 6.5 TB/s; one over 131072: 82 us and a
-// merge of 6.
+// the end.  A weight is the sum of two bf16 parts, each multiplied by the
+// values, so 16 bits of it count, as in the decode over an index.  With up to
+// eight rows (a token of a group of eight heads) the second parts are the
+// operand's rows 8..15, so a tile takes as many products as with weights of
+// one part (363 us against 361 for 16 tokens over 32768 keys each; with
+// products of their own 373: the clocks fall under the power cap).  A tile
+// costs a warp about 250 instructions, a third of the time its 64 KB take to
+// arrive, and a stage is free as soon as eight warps have read it: the
+// tensor-memory kernel holds its stages through a softmax of 128 rows, which
+// leaves 96 KB in flight and 4.9 TB/s.  16 tokens over 32768 keys each, 8 KV
+// heads of 128: 363 us a call back to back, 5.9 TB/s; one over 131072: 93 us,
+// 6 of them the merge.
 #include <cmath>
 
 #include "wi_attend_tiles.cuh"
@@ -65,6 +71,7 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
   }
   const int G = 1 << tb.g_shift, n = it.t1 - it.t0;
   const int first_pos = it.pos0 + (it.row0 >> tb.g_shift);
+  const bool narrow = it.rows <= kFewRows / 2;   // accumulator rows 8..15: the weights' second parts
   __syncthreads();
   if (warp == kFewWarps) {
     load_units<D, S::kStages>(it, tb.hkv, kp, vp, map_k, map_v, ring, s_full, s_empty, status);
@@ -131,10 +138,11 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
         for (int e = 0; e < 4; ++e)
           if (base + 8 * nt + t2 + (e & 1) > pos[e >> 1]) s[nt][e] = -INFINITY;
     }
-    float top[2];
+    float top[2] = {-INFINITY, -INFINITY};
     bool up = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (h == 1 && narrow) break;
       float x = max3_nan(s[0][2 * h], s[0][2 * h + 1], max3_nan(s[1][2 * h], s[1][2 * h + 1], s[1][2 * h]));
 #pragma unroll
       for (int y = 1; y <= 2; y <<= 1) {
@@ -158,10 +166,11 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
 #pragma unroll
       for (int x = 0; x < D / 8; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][e] *= c[e >> 1];
+        for (int e = 0; e < 4; ++e) o[x][e] *= e < 2 || narrow ? c[0] : c[1];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (h == 1 && narrow) break;
       const float mu = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -172,8 +181,16 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
           l[h] += x;
         }
     }
-    const uint32_t a0 = pack_bf16(s[0][0], s[0][1]), a1 = pack_bf16(s[0][2], s[0][3]);
-    const uint32_t a2 = pack_bf16(s[1][0], s[1][1]), a3 = pack_bf16(s[1][2], s[1][3]);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) split_bf16(s[e >> 1][0], s[e >> 1][1], hi[e], lo[e]);
+    if (narrow) {
+      hi[1] = lo[0];
+      hi[3] = lo[2];
+    } else {
+#pragma unroll
+      for (int e = 1; e < 4; e += 2) split_bf16(s[e >> 1][2], s[e >> 1][3], hi[e], lo[e]);
+    }
     if (!(ok = full())) break;
     {
       const unsigned char* tile = ring + (size_t)st * S::kTile;
@@ -187,11 +204,21 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
 #pragma unroll
           for (int e = 0; e < 4; ++e) b[e] = clean(b[e], base + t2 + 8 * (e & 1), first_pos, it.key_end, bad);
         }
-        mma_bf16_4(o[2 * cb], a0, a1, a2, a3, b[0], b[1]);
-        mma_bf16_4(o[2 * cb + 1], a0, a1, a2, a3, b[2], b[3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mma_bf16_4(o[2 * cb + e], hi[0], hi[1], hi[2], hi[3], b[2 * e], b[2 * e + 1]);
+        if (!narrow) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mma_bf16_4(o[2 * cb + e], lo[0], lo[1], lo[2], lo[3], b[2 * e], b[2 * e + 1]);
+        }
       }
     }
     release();
+  }
+  if (narrow) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o[c][e] += o[c][e + 2];
   }
   // join the warps' parts in the ring's memory (every unit has been read)
 #pragma unroll
@@ -230,19 +257,30 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
       const float4 f = *reinterpret_cast<const float4*>(so + (w * kFewRows + r) * D + col);
       v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
     }
-    if (s_bad) {
-      // values that are not finite, to the rows that see them (a positive
-      // weight of them is they themselves)
+    // A value that is not finite, under a positive weight, is all there is to
+    // its column: those taken out on the diagonal, and where the sum is not
+    // finite, the others too (a weight's second part, 0 or negative, makes NaN
+    // of an infinity).  A row whose mass is NaN is NaN whatever they are.
+    const bool lost = mass == mass && !(isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]));
+    if (s_bad || lost) {
       const int p1 = min(it.pos0 + (row >> tb.g_shift) + 1, it.t1 * kRows);
+      float odd[4] = {};
+      uint32_t found = 0;
 #pragma unroll 1
-      for (int p = max(first_pos + 1, it.t0 * kRows); p < p1; ++p) {
+      for (int p = max(lost ? 0 : first_pos + 1, it.t0 * kRows); p < p1; ++p) {
         const int64_t at = pool_row(vp, tb.hkv, D, it.b, it.h, p, status);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float f = at < 0 ? 0.f : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(vp.base)[at + col + e]);
-          if (!isfinite(f)) v[e] += f;
+          if (!isfinite(f)) {
+            odd[e] += f;
+            found |= 1u << e;
+          }
         }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((found >> e) & 1u) v[e] = odd[e];
     }
     if (it.part >= 0) {
       if (col == 0) ao.ml[it.part + r] = make_float2(mx, mass);

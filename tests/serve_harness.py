@@ -80,24 +80,27 @@ def attend_reference(q, k_pool, v_pool, table, lens, q_lens):
     return out, lse, mag, dot
 
 
-def attend_bounds(out, lse, mag, dot, dtype, T, d):
+def attend_bounds(out, lse, mag, dot, dtype, T, d, weight=None):
     """Error bounds from the arithmetic.  A score is d exact (bf16) or rounded
     products added in fp32, at most 2^-23 relative an addition, then one
     scaling: |ds| <= (d + 4) 2^-23 dot.  2^x is taken to within 2^-20.  A
     weight is then off by ds + 2^-20 relative, and by a rounding to the
-    storage type on the way to the product with the values (bf16).  The mass
+    storage type on the way to the product with the values (bf16; `weight`:
+    the rounding of a weight where it is another).  The mass
     and the output add T terms in fp32 (T 2^-23).  The output divides by the
     mass, so both errors count, and is rounded once."""
     w = (d + 4) * 2.0 ** -23 * dot + 2.0 ** -20 + T * 2.0 ** -23
     rounded = U[torch.bfloat16] if dtype == torch.bfloat16 else 0.0
+    if weight is not None:
+        rounded = weight
     tol_out = (2 * w[..., None] + rounded) * mag * 1.01 + U[dtype] * np.abs(out) + 1e-30
     tol_lse = w + 2.0 ** -22 * (1 + np.abs(lse))
     return tol_out, tol_lse
 
 
-def assert_attend(got_out, got_lse, ref, dtype, T, d):
+def assert_attend(got_out, got_lse, ref, dtype, T, d, weight=None):
     out, lse, mag, dot = ref
-    tol_out, tol_lse = attend_bounds(out, lse, mag, dot, dtype, T, d)
+    tol_out, tol_lse = attend_bounds(out, lse, mag, dot, dtype, T, d, weight)
     err = np.abs(got_out.detach().cpu().double().numpy()[:len(out)] - out)
     assert (err <= tol_out).all(), f"out: {np.nanmax(err / tol_out)} of the bound, {np.isnan(err).sum()} NaN"
     err = np.abs(got_lse.detach().cpu().double().numpy()[:len(out)] - lse)

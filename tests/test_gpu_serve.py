@@ -472,6 +472,43 @@ def test_tensors_on_another_device_than_the_current_one():
     assert out.device.index == 1 and torch.equal(out.to(DEV), want)
 
 
+# A weight as two bf16 parts: the second is the rest of the first, off by half
+# a step of itself, so by 2^-8 * 2^-8 of the weight.
+TWO_PARTS = S.U[BF16] ** 2
+
+
+@pytest.mark.parametrize("lens,q_lens,H,G,d", [
+    ([2], [1], 4, 8, 128), ([3, 5], [1, 2], 4, 8, 64), ([18], [16], 4, 1, 128), ([1500, 4], [2, 2], 2, 8, 128),
+])
+def test_attend_few_rows_keep_16_bits_of_a_weight(lens, q_lens, H, G, d):
+    """Few keys of about equal weight: where the values nearly cancel, a weight
+    rounded to bf16 is many times the bound."""
+    kv = make_cache(lens, H, d, 16, BF16, 31, spread=0.3)
+    q = make_q(sum(q_lens), H * G, d, BF16, 31)
+    out, lse = W.attend(q, kv, W.AttendParams(H * G, q_lens))
+    ref = S.attend_reference(q, kv.k_pool, kv.v_pool, kv.block_table, lens, q_lens)
+    S.assert_attend(out, lse, ref, BF16, max(lens), d, TWO_PARTS)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("T,n,G", [(300, 1, 4), (1500, 3, 4), (1500, 12, 1), (700, 40, 4)])
+def test_attend_value_that_is_not_finite_and_all_see(dtype, bad, T, n, G):
+    kv = make_cache([T], 2, 128, 16, dtype, 35, spread=0.3)
+    q = make_q(n, 2 * G, 128, dtype, 35)
+    clean, clean_lse = W.attend(q, kv, W.AttendParams(2 * G, [n]))
+    for at in (3, T // 2):
+        kv.v_pool[int(kv.block_table[0, at // 16]), 1, at % 16, 7] = bad
+    kv.v_pool[int(kv.block_table[0, 0]), 1, 4, 9] = -bad
+    out, lse = W.attend(q, kv, W.AttendParams(2 * G, [n]))
+    assert torch.equal(lse, clean_lse) and torch.equal(out[:, :G], clean[:, :G])
+    for c, want in ((7, bad), (9, -bad)):
+        hit = out[:, G:, c]
+        assert (hit == want).all() if bad == bad else torch.isnan(hit).all()
+    rest = [c for c in range(128) if c not in (7, 9)]
+    assert torch.equal(out[:, G:, rest], clean[:, G:, rest])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
