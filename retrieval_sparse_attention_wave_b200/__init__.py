@@ -112,7 +112,7 @@ class WiKVAppend(C.Structure):
 
 class WiAttendParams(C.Structure):
     _fields_ = [("n_q_heads", C.c_int32), ("q_lens", C.POINTER(C.c_int32)),
-                ("q_stride", C.c_int64), ("out_stride", C.c_int64)]
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64), ("exact_weights", C.c_int32)]
 
 
 _P = C.c_void_p
@@ -776,9 +776,12 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
 @dataclass
 class AttendParams:
     """q_lens[b]: query tokens of sequence b, its last ones (None: all of them).
-    The list is read when the object is made."""
+    The list is read when the object is made.  exact_weights: 16 bits of every
+    softmax weight in bf16 calls of many rows too (a third more time; see
+    wi_attend in include/wi.h)."""
     n_q_heads: int
     q_lens: Optional[List[int]] = None
+    exact_weights: bool = False
 
     def __post_init__(self):
         self._q_lens = None if self.q_lens is None else _i32_array(self.q_lens)
@@ -793,7 +796,8 @@ class AttendParams:
         return self._total
 
     def c_struct(self, q_stride: int = 0, out_stride: int = 0) -> WiAttendParams:
-        return WiAttendParams(self.n_q_heads, self._q_ptr, q_stride, out_stride)
+        return WiAttendParams(self.n_q_heads, self._q_ptr, q_stride, out_stride,
+                              1 if self.exact_weights else 0)
 
 
 def attend_workspace_bytes(kv: KVCache, params: AttendParams) -> int:

@@ -7,7 +7,12 @@
 //   O_i += P_i V_j     (P_i straight from tensor memory).
 // The weights are rounded to bf16, the type of the values they multiply (half
 // a step, 2^-8 of a weight, averages out over the keys; the output's own
-// rounding is as large); their sum is taken before that, in fp32.
+// rounding is as large); their sum is taken before that, in fp32.  Where the
+// caller asks for exact_weights, a weight is two bf16 parts (P_i and the rest
+// of it, in the other half of S_i's columns) and 16 bits of it count: a third
+// more time (8192 tokens 679 us against 526, 32768 10.4 ms
+// against 7.9) for an output off by its own rounding alone
+// (relative 0.0016 against 0.0022).
 // Roles:
 //   warps 0..3, 4..7  softmax of query tile 0, 1: a thread owns a row
 //                     (a tensor-memory lane), so its maximum, mass and output
@@ -124,7 +129,7 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-template <int D, int N>
+template <int D, int N, bool kExact>
 __global__ void __launch_bounds__(kUThreads, 1)
 attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -215,6 +220,8 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
             const int k = half * (kRows / 32) + kk;
             umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
                          !first || kk != 0);
+            if (kExact)   // the weights' second parts
+              umma_bf16_ts(tmem + S::kO + i * D, tmem + S::kS + i * 128 + 64 + k * 8, b + k * (2048 >> 4), kIdescO, true);
           }
           if (half == 1) {
             umma_commit(&s_o[i]);
@@ -376,15 +383,17 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
+            uint32_t p[16], p2[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc, nm);
               const float2 w = e % kPoly == kPoly - 1 ? ex2_poly(y) : make_float2(ex2(y.x), ex2(y.y));
               sum[e & 1] = __fadd2_rn(sum[e & 1], w);
-              p[e] = pack_bf16(w.x, w.y);
+              if (kExact) split_bf16(w.x, w.y, p[e], p2[e]);
+              else p[e] = pack_bf16(w.x, w.y);
             }
             tmem_st16(ts + 16 * c, p);
+            if (kExact) tmem_st16(ts + 64 + 16 * c, p2);
             if (c == 1) {   // the product over the first half may start
               tmem_wait_st();
               tc_fence_before();
@@ -423,10 +432,15 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
       const bool part = it.part >= 0;
       const int r4 = r - lane + (lane & ~3);
       uint4 x[4];
+      bool lost = false;   // a sum is not finite (exact_weights)
 #pragma unroll 1
       for (int col = 0; col < D; col += 16) {
         uint32_t y[16];
         tmem_ld16(to + col, y);
+        if (kExact) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) lost |= !isfinite(__uint_as_float(y[e]));
+        }
         if (part) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
@@ -451,23 +465,36 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
           *reinterpret_cast<uint4*>(o + 16 * (lane & 3)) = t[c];
         }
       }
-      if (*(volatile uint32_t*)&s_bad != 0) {
-        // values that are not finite, added to the rows that see them (a
-        // positive weight of them is they themselves)
+      lost = lost && real && l == l;   // (a row whose mass is NaN is NaN)
+      if (__any_sync(0xffffffffu, lost || *(volatile uint32_t*)&s_bad != 0)) {
+        // Values that are not finite, added to the rows that see them (a
+        // positive weight of them is they themselves).  With weights of two
+        // parts, the second 0 or negative, an infinity that every row sees has
+        // made NaN of its column: all of a lost row's keys are looked at, and
+        // the first such value takes its column's place.
         __syncwarp();
         const int p1 = real ? min(pos + 1, it.t1 * kRows) : 0;
+        uint32_t found[D / 32] = {};
 #pragma unroll 1
-        for (int p = max(first_pos + 1, it.t0 * kRows); p < p1; ++p) {
+        for (int p = max(lost ? 0 : first_pos + 1, it.t0 * kRows); p < p1; ++p) {
           const int64_t at = pool_row(vp, tb.hkv, D, it.b, it.h, p, status);
 #pragma unroll 1
           for (int c = 0; at >= 0 && c < D; ++c) {
-            const float f = __bfloat162float(reinterpret_cast<const T*>(vp.base)[at + c]);
+            const T* v = reinterpret_cast<const T*>(vp.base) + at + c;
+            if (c % 8 == 0 && !nonfinite(*reinterpret_cast<const uint4*>(v))) {
+              c += 7;
+              continue;
+            }
+            const float f = __bfloat162float(*v);
             if (isfinite(f)) continue;
+            const bool first = kExact && !((found[c / 32] >> (c % 32)) & 1u);
+            found[c / 32] |= 1u << (c % 32);
             if (part) {
-              ao.o[(it.part + r) * D + c] += f;
+              float* o = ao.o + (it.part + r) * D + c;
+              *o = first ? f : *o + f;
             } else {
               T* o = out_row(r) + c;
-              *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
+              *o = __float2bfloat16_rn(first ? f : __bfloat162float(*o) + f);
             }
           }
         }
@@ -482,7 +509,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
   }
 }
 
-template <int D, int N>
+template <int D, bool kExact, int N>
 cudaError_t launch_typed(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a, const AttendOut& ao,
                          cudaStream_t s) {
   using S = UmmaShape<D>;
@@ -493,9 +520,9 @@ cudaError_t launch_typed(const AttendTable<N>& tb, const AttendPlan& pl, const A
   const cuuint32_t qb[3] = {64, (cuuint32_t)pl.G, (cuuint32_t)(kRows / pl.G)};
   if (!encode_map(&mq, 3, a.q, qd, qs, qb) || !encode_pools(&mk, &mv, a, pl.hkv, D))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<attend_umma_kernel<D, N>>(S::kSmem);
+  const cudaError_t e = allow_smem<attend_umma_kernel<D, N, kExact>>(S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attend_umma_kernel<D, N>, dim3(tb.n_items), kUThreads, S::kSmem, s, false, tb, mq, mk, mv, a.kp,
+  return launch_kernel(attend_umma_kernel<D, N, kExact>, dim3(tb.n_items), kUThreads, S::kSmem, s, false, tb, mq, mk, mv, a.kp,
                        a.vp, ao, kLog2e / std::sqrt((float)D), reinterpret_cast<uint32_t*>(a.ws));
 }
 
@@ -504,7 +531,8 @@ cudaError_t launch_typed(const AttendTable<N>& tb, const AttendPlan& pl, const A
 template <int N>
 cudaError_t launch_attend_umma(const AttendTable<N>& tb, const AttendPlan& pl, const AttendArgs& a,
                              const AttendOut& ao, cudaStream_t s) {
-  return pl.D == 128 ? launch_typed<128>(tb, pl, a, ao, s) : launch_typed<64>(tb, pl, a, ao, s);
+  if (pl.exact) return pl.D == 128 ? launch_typed<128, true>(tb, pl, a, ao, s) : launch_typed<64, true>(tb, pl, a, ao, s);
+  return pl.D == 128 ? launch_typed<128, false>(tb, pl, a, ao, s) : launch_typed<64, false>(tb, pl, a, ao, s);
 }
 template cudaError_t launch_attend_umma(const AttendTable<kFewSeqs>&, const AttendPlan&, const AttendArgs&,
                                       const AttendOut&, cudaStream_t);

@@ -305,6 +305,7 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
     if (s != 0 && (s < row || s % vec != 0)) return WI_ERR_INVALID_ARG;
   std::memset(&pl, 0, sizeof(pl));
   pl.hkv = H; pl.G = G; pl.Hq = p->n_q_heads; pl.D = kv->head_dim; pl.dtype = kv->dtype;
+  pl.exact = p->exact_weights != 0;
   int q0 = 0, most = 0;
   for (int b = 0; b < kv->batch; ++b) {
     const int T = kv->seq_lens[b], n = p->q_lens ? p->q_lens[b] : T;

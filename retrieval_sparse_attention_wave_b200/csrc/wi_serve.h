@@ -58,6 +58,7 @@ struct AttendPlan {
   int n_seq;        // sequences with query tokens, the longest key range first
   int n_items, n_merge_rows;
   int hkv, G, Hq, D, dtype;
+  bool exact;       // 16 bits of a softmax weight (bf16)
   int rows, keys;   // rows per block, keys per tile
   int64_t q_tokens; // rows of the packed q
   size_t off_ml, off_o, total;   // workspace: {m, l} and o of the part rows

@@ -509,6 +509,43 @@ def test_attend_value_that_is_not_finite_and_all_see(dtype, bad, T, n, G):
     assert torch.equal(out[:, G:, rest], clean[:, G:, rest])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,q_lens,H,G", [
+    ([20], [20], 2, 1), ([5, 40], [5, 17], 2, 4), ([300], [300], 1, 1), ([130, 0, 9], [70, 0, 9], 2, 8),
+    ([2600], [70], 1, 4), ([700, 690], [1, 300], 2, 2),
+])
+def test_attend_exact_weights(d, lens, q_lens, H, G):
+    """16 bits of a weight at the caller's wish: queries with few keys of about
+    equal weight, blocks of 128 and 256 rows, split and not."""
+    kv = make_cache(lens, H, d, 16, BF16, 37, spread=0.3)
+    q = make_q(sum(q_lens), H * G, d, BF16, 37)
+    out, lse = W.attend(q, kv, W.AttendParams(H * G, q_lens, exact_weights=True))
+    ref = S.attend_reference(q, kv.k_pool, kv.v_pool, kv.block_table, lens, q_lens)
+    S.assert_attend(out, lse, ref, BF16, max(lens), d, TWO_PARTS)
+    other, other_lse = W.attend(q, kv, W.AttendParams(H * G, q_lens))
+    assert torch.equal(other_lse, lse)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("T,n", [(300, 300), (1500, 40), (900, 70)])
+def test_attend_exact_weights_with_values_that_are_not_finite(bad, T, n):
+    kv = make_cache([T], 2, 128, 16, BF16, 39, spread=0.3)
+    q, prm = make_q(n, 8, 128, BF16, 39), W.AttendParams(8, [n], exact_weights=True)
+    clean, clean_lse = W.attend(q, kv, prm)
+    late = T - n // 2                      # half of the queries see it, and all see key 3 but a prompt's first
+    for at, c in ((3, 7), (late, 9)):
+        kv.v_pool[int(kv.block_table[0, at // 16]), 1, at % 16, c] = bad
+    out, lse = W.attend(q, kv, prm)
+    assert torch.equal(lse, clean_lse) and torch.equal(out[:, :4], clean[:, :4])
+    for at, c in ((3, 7), (late, 9)):
+        i = max(0, at - (T - n))
+        assert torch.equal(out[:i, :, c], clean[:i, :, c])
+        hit = out[i:, 4:, c]
+        assert (hit == bad).all() if bad == bad else torch.isnan(hit).all()
+    rest = [c for c in range(128) if c not in (7, 9)]
+    assert torch.equal(out[:, 4:, rest], clean[:, 4:, rest])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
