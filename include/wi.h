@@ -487,7 +487,8 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * softmax weights rounded to bf16 for the product with the values (relative
  * error of the output 0.0022, 0.0016 from its own rounding); exact_weights keeps
  * 16 bits of them, as calls of fewer rows always do, for about a third more
- * time.  The weights' sum and the accumulators are fp32.  A block-table entry outside the pool reads as zero
+ * time.  The weights' sum and the accumulators are fp32; finite values have a
+ * finite output as long as the sum of a channel's |v| is below 2^127.  A block-table entry outside the pool reads as zero
  * rows and sets WI_DEV_BAD_PAGE.  Sequences with few query rows have their
  * keys split over the SMs and joined in a fixed order: results do not change
  * from run to run.  Workspace: wi_attend_workspace_size for the same cache

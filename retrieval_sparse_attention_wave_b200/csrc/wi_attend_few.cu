@@ -26,7 +26,7 @@ namespace wi {
 namespace {
 
 constexpr int kFewRows = 16, kFewWarps = 8, kFewThreads = 32 * (kFewWarps + 1);
-constexpr float kFewRescale = 24.f;   // log2 of the growth that forces a rescale
+constexpr float kFewHead = 24.f;   // log2 of the reference's distance above the maximum it was set at (weights at most 1)
 
 template <int D>
 struct FewShape {
@@ -152,13 +152,13 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
       // a score that is NaN or +inf makes its row NaN
       x *= scale;
       top[h] = x < INFINITY ? x : NAN;
-      up |= !(top[h] <= m[h] + kFewRescale);
+      up |= !(top[h] <= m[h]);
     }
     if (__any_sync(0xffffffffu, up)) {
       float c[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float mn = !(top[h] <= m[h] + kFewRescale) ? top[h] : m[h];
+        const float mn = !(top[h] <= m[h]) ? top[h] + kFewHead : m[h];
         c[h] = mn == m[h] ? 1.f : ex2(m[h] - mn);
         m[h] = mn;
         l[h] *= c[h];

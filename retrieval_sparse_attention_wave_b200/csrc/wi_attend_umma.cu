@@ -27,9 +27,11 @@
 //                     some queries see (weight 0 times them is not 0) are
 //                     taken out and given back to those that see them at the
 //                     end.
-// The output is rescaled only when a row's maximum rises by more than 2^24:
-// the reference point m only keeps the powers in range, P and the mass being
-// relative to the same m whatever it is.
+// The reference point m only keeps the powers in range, P and the mass being
+// relative to the same m whatever it is.  It is set 2^24 above a row's maximum
+// and moves when the maximum passes it, so the output is seldom rescaled, and
+// weights stay at or below 1: the sums are finite as long as tokens x |v| is.
+// (Their last bits are lost for |v| below 2^-100.)
 //
 // What bounds it: a group's own chain.  A tile's softmax takes about 1650
 // clocks (read 170, maximum 250, weights 1220: the special-function unit
@@ -47,10 +49,10 @@ namespace wi {
 namespace {
 
 constexpr int kUThreads = 384;
-// log2 of the growth that forces a rescale: the output's sums stay finite while
-// tokens x |v| < 2^103.  At 2^8 rescales are common in a sequence's first
-// tiles: short prompts took 22.5 us against 20.5.
-constexpr float kRescale = 24.f;
+// log2 of the reference's distance above the maximum it was set at.  At 2^8
+// rescales are common in a sequence's first tiles: short prompts took 22.5 us
+// against 20.5.
+constexpr float kHead = 24.f;
 // Every kPoly-th pair of weights is taken without the special-function unit.
 // 8192 tokens: 2 takes 480 us, 3 444, 4 441, 8 445.
 constexpr int kPoly = 4;
@@ -365,9 +367,9 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
           // a score that is NaN or +inf makes its row NaN
           float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale;
           top = top < INFINITY ? top : NAN;
-          const bool up = !(top <= m + kRescale);
+          const bool up = !(top <= m);
           if (__any_sync(0xffffffffu, up)) {
-            const float mn = up ? top : m;
+            const float mn = up ? top + kHead : m;
             const float c = up ? ex2(m - mn) : 1.f;
             l *= c;
             m = mn;

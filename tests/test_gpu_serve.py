@@ -2,6 +2,8 @@
 and appends exactly, attention within the bounds of its arithmetic
 (serve_harness.attend_bounds), and all of them together with the index build
 and decode."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -544,6 +546,37 @@ def test_attend_exact_weights_with_values_that_are_not_finite(bad, T, n):
         assert (hit == bad).all() if bad == bad else torch.isnan(hit).all()
     rest = [c for c in range(128) if c not in (7, 9)]
     assert torch.equal(out[:, 4:, rest], clean[:, 4:, rest])
+
+
+def steps_cache(T, d, dtype, seed, rise):
+    """Scores 0 and `rise` (base 2) in turns of 128 keys for a query of ones in
+    channel 0: a maximum that a block meets late."""
+    kv = make_cache([T], 1, d, 16, dtype, seed)
+    pos = torch.arange(T, device=DEV)
+    pages, rows = kv.block_table[0].long()[pos // 16], pos % 16
+    k = torch.zeros(T, 1, d, device=DEV)
+    k[:, 0, 0] = torch.where(pos % 256 < 128, 0.0, rise * math.sqrt(d) * math.log(2))
+    kv.k_pool[pages, :, rows] = k.to(dtype)
+    return kv
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("q_len", [1, 4, 20, 260])
+@pytest.mark.parametrize("rise", [22, 40])
+@pytest.mark.parametrize("exact", [False, True])
+def test_attend_range_of_values(dtype, q_len, rise, exact):
+    """Values up to 2^114 (900 of them stay below 2^127) and down to 2^-90."""
+    T, d, G = 900, 64, 4
+    kv = steps_cache(T, d, dtype, 33, rise)
+    q = torch.zeros(q_len, G, d, device=DEV)
+    q[:, :, 0] = 1
+    q, prm = q.to(dtype), W.AttendParams(G, [q_len], exact_weights=exact)
+    ref = S.attend_reference(q, kv.k_pool, kv.v_pool, kv.block_table, [T], [q_len])
+    v = kv.v_pool.clone()
+    for power in (112, -90):
+        kv.v_pool.copy_((v.double() * 2.0 ** power).to(dtype))
+        out, lse = W.attend(q, kv, prm)
+        S.assert_attend(out.double() * 2.0 ** -power, lse, ref, dtype, T, d)
 
 
 # ---------------------------------------------------------------- together
