@@ -25,11 +25,11 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // thread takes four packed tokens at a time: a search of the starts in shared
 // memory, the slot from the table (a page in use) or straight from the stack
 // (a page this call hands out, whose table entry another CTA may be writing),
-// and 16-byte stores.  The lengths and the stack's size may be updated in
-// place, so the CTA that arrives last, when every CTA has read them, writes
-// them; the arrival counter lives in the workspace's status block and is
-// zero again when the call ends.  Latency bounds it (lengths, scan, page,
-// store): 7.6 us for a step of 64 requests, cold; 335445 tokens 6.0 us.
+// and 16-byte stores.  The first CTA writes the lengths and the stack's size
+// too; where they are updated in place and other CTAs may still be reading
+// them, a kernel of one CTA behind this one does.  Nothing is kept between
+// calls.  Latency bounds it (lengths, scan, page, store): 7.6 us for a step of
+// 64 requests, cold; 335445 tokens 6.0 us.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 4 * kPlanThreads;   // per CTA and round
 
@@ -38,7 +38,7 @@ struct PlanArgs {
   const int32_t *seq_lens, *new_lens, *free_pages, *n_free;
   int32_t *block_table, *seq_lens_out, *n_free_out, *starts, *slot_map, *positions;
   uint32_t* status;
-  uint32_t* arrivals;
+  bool write_lens;   // plan_pages_kernel writes seq_lens_out and n_free_out
 };
 
 // the last i < n with tab[i] <= x (tab ascending, tab[0] <= x)
@@ -51,8 +51,17 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* tab, int n, int x
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs a) {
-  __shared__ int32_t s_start[kMaxBatch + 1], s_need[kMaxBatch + 1], s_have[kMaxBatch];
+// The step as each of a CTA's threads needs it: its request's lengths (thread
+// tid < batch), the new tokens and pages of the requests before it, and the
+// sums.  A step that does not fit has no new tokens and no pages.
+struct PlanStep {
+  int32_t have, fresh;
+  int32_t start, taken;
+  int32_t tokens, pages, n_free;
+  uint32_t bad;
+};
+
+__device__ __forceinline__ PlanStep plan_step(const PlanArgs& a) {
   __shared__ int64_t s_sum[2][kPlanThreads / 32];
   __shared__ uint32_t s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -69,13 +78,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
     uint32_t bad = 0;
     if (have < 0 || fresh < 0 || have + fresh > INT32_MAX) {
       bad = WI_DEV_BAD_SLOT;
-      have = fresh = 0;
+      fresh = 0;
     }
     const int64_t pages = (have + fresh + page_mask) >> a.page_shift;
     need = pages - ((have + page_mask) >> a.page_shift);
     if (pages > a.max_pages) bad |= WI_DEV_NO_PAGES;
     if (bad) atomicOr(&s_bad, bad);
-    s_have[tid] = (int32_t)have;
   }
   int64_t x = fresh, y = need;   // inclusive scans
 #pragma unroll
@@ -84,7 +92,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
     if (lane >= o) { x += px; y += py; }
   }
   if (lane == 31) { s_sum[0][warp] = x; s_sum[1][warp] = y; }
-  __syncthreads();
+  __syncthreads();   // and every thread of this CTA has read the lengths
   int64_t all_fresh = 0, all_need = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
@@ -96,31 +104,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
   if (n_free < 0 || n_free > a.max_free) bad |= WI_DEV_BAD_PAGE;
   else if (all_need > n_free || all_fresh > a.capacity) bad |= WI_DEV_NO_PAGES;
   if (bad) { all_fresh = all_need = 0; x = y = fresh = need = 0; }
+  return PlanStep{(int32_t)have, (int32_t)fresh, (int32_t)(x - fresh), (int32_t)(y - need),
+                  (int32_t)all_fresh, (int32_t)all_need, n_free, bad};
+}
+
+__device__ __forceinline__ void write_lens(const PlanArgs& a, const PlanStep& st) {
+  if ((int)threadIdx.x < a.batch) a.seq_lens_out[threadIdx.x] = st.have + st.fresh;
+  if (threadIdx.x == 0) *a.n_free_out = st.n_free - st.pages;
+}
+
+// The lengths and the stack's size in place, behind a plan_pages_kernel of
+// several CTAs.
+__global__ void __launch_bounds__(kPlanThreads) plan_advance_kernel(const PlanArgs a) {
+  pdl_wait();   // every CTA of the plan has ended
+  write_lens(a, plan_step(a));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs a) {
+  __shared__ int32_t s_start[kMaxBatch + 1], s_need[kMaxBatch + 1], s_have[kMaxBatch];
+  const int tid = threadIdx.x;
+  const int page_mask = (1 << a.page_shift) - 1;
+  pdl_launch_dependents();
+  const PlanStep st = plan_step(a);
+  const int total = st.tokens, n_need = st.pages, n_free = st.n_free;
   if (tid < a.batch) {
-    s_start[tid] = (int32_t)(x - fresh);
-    s_need[tid] = (int32_t)(y - need);
+    s_have[tid] = st.have;
+    s_start[tid] = st.start;
+    s_need[tid] = st.taken;
   }
-  const int total = (int)all_fresh, n_need = (int)all_need;
   if (tid == 0) { s_start[a.batch] = total; s_need[a.batch] = n_need; }
-  __syncthreads();   // every thread of this CTA has read its lengths
-  if (tid == 0) {
-    bool last = gridDim.x == 1;
-    if (!last) {
-      fence_acq_rel_gpu();
-      last = atomicAdd(a.arrivals, 1u) == gridDim.x - 1;
-      fence_acq_rel_gpu();
-    }
-    s_bad = last ? 1u : 0u;
-    if (last) *a.arrivals = 0;
-    if (bad && blockIdx.x == 0) flag_error(a.status, bad);
-  }
   __syncthreads();
-  if (s_bad) {
-    if (tid < a.batch) a.seq_lens_out[tid] = bad ? a.seq_lens[tid] : (int32_t)(have + fresh);
-    if (tid == 0) *a.n_free_out = n_free - n_need;
-  }
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
+    if (a.write_lens) write_lens(a, st);
+    if (tid == 0 && st.bad) flag_error(a.status, st.bad);
     for (int i = tid; i <= a.batch; i += kPlanThreads) a.starts[i] = s_start[i];
+  }
 
   uint32_t flags = 0;
   // a page off the stack, or -1
@@ -357,12 +375,15 @@ wi_status check_ws(const void* ws, size_t have, size_t need) {
 }  // namespace
 
 cudaError_t launch_plan_pages(const wi_page_plan& p, unsigned char* ws, cudaStream_t s) {
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(p.capacity, kPlanTokens), 4 * 148));
+  const bool in_place = p.seq_lens_out == p.seq_lens || p.n_free_out == p.n_free;
   PlanArgs a{p.batch, ilog2(p.page_size), (int32_t)p.n_pages, p.max_pages, p.max_free, p.capacity,
              aligned(p.slot_map, 16) && aligned(p.positions, 16), p.seq_lens, p.new_lens, p.free_pages,
              p.n_free, p.block_table, p.seq_lens_out, p.n_free_out, p.starts, p.slot_map, p.positions,
-             reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 64)};
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(p.capacity, kPlanTokens), 4 * 148));
-  return launch_kernel(plan_pages_kernel, dim3(grid), kPlanThreads, 0, s, false, a);
+             reinterpret_cast<uint32_t*>(ws), grid == 1 || !in_place};
+  const cudaError_t e = launch_kernel(plan_pages_kernel, dim3(grid), kPlanThreads, 0, s, false, a);
+  if (e != cudaSuccess || a.write_lens) return e;
+  return launch_kernel(plan_advance_kernel, dim3(1), kPlanThreads, 0, s, true, a);
 }
 
 cudaError_t launch_append_kv(const wi_kv_append& p, unsigned char* ws, cudaStream_t s) {

@@ -143,6 +143,50 @@ def test_plan_page_outside_the_pool():
     assert W.read_device_status(ws) == W.WI_DEV_BAD_PAGE
 
 
+@pytest.mark.parametrize("left", [0, 1, 255])
+def test_plans_of_many_tokens_in_place_keep_nothing_in_the_workspace(left):
+    """Plans of 1 to 12 blocks on one workspace, whatever an ended call left
+    behind the status word: the lengths advance and the workspace stays."""
+    table = make_table([0] * 5, 16, 3000, 800, 61)
+    ws = W.workspace(512, DEV)
+    ws[4:].fill_(left)
+    for new in ([1000, 17, 2000, 0, 5], [1] * 5, [3000, 3000, 1, 1, 6000], [400, 0, 0, 0, 625], [0, 0, 0, 1024, 1]):
+        before = table.seq_lens.tolist()
+        check_plan(table, new, sum(new) + 3, update=True, ws=ws)
+        assert table.seq_lens.tolist() == [h + n for h, n in zip(before, new)]
+        assert (ws[4:] == left).all()
+    check_plan(table, [1, 2, 3, 4, 5000], 5000, update=True, ws=ws)     # over the capacity: as it was
+    assert W.read_device_status(ws) == W.WI_DEV_NO_PAGES
+
+
+def test_plan_in_place_of_one_of_the_two():
+    for keep in ("seq_lens", "n_free"):
+        table = make_table([9, 0], 16, 400, 200, 63)
+        out = W.PagePlan.empty(table, 2600)
+        setattr(out, keep, getattr(table, keep))
+        check_plan(table, [2500, 99], 2600, out=out)
+
+
+def test_plan_of_many_tokens_captured_in_place():
+    table = make_table([30, 0, 17], 16, 900, 400, 65)
+    new = i32([700, 0, 600])
+    plan = W.PagePlan.empty(table, 1300, update=True)
+    ws = W.serve_workspace(DEV)
+    ref_table = table.block_table.tolist()
+    lens, stack, n_free = table.seq_lens.tolist(), table.free_pages.tolist(), int(table.n_free)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        W.plan_pages(table, new, 1300, out=plan, update=True, ws=ws)
+    for _ in range(4):
+        ref_table, slots, _, _, lens, n_free = S.plan_reference(
+            ref_table, lens, [700, 0, 600], stack, n_free, 16, 900, 1300)
+        g.replay()
+        assert plan.slot_map.tolist() == slots
+        assert table.seq_lens.tolist() == lens and int(table.n_free) == n_free
+    assert table.block_table.tolist() == ref_table
+
+
 # ---------------------------------------------------------------- appends
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
