@@ -51,6 +51,11 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* tab, int n, int x
   return lo;
 }
 
+// The pages of `have` tokens (which may be all an int holds).
+__device__ __forceinline__ int pages_of(int have, int page_shift) {
+  return (have >> page_shift) + ((have & ((1 << page_shift) - 1)) != 0);
+}
+
 // The step as each of a CTA's threads needs it: its request's lengths (thread
 // tid < batch), the new tokens and pages of the requests before it, and the
 // sums.  A step that does not fit has no new tokens and no pages.
@@ -149,9 +154,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
     return -1;
   };
   const int stride = gridDim.x * kPlanThreads;
-  for (int e = blockIdx.x * kPlanThreads + tid; e < n_need; e += stride) {
-    const int b = last_at_or_below(s_need, a.batch, e);
-    const int lp = ((s_have[b] + page_mask) >> a.page_shift) + (e - s_need[b]);
+  for (int64_t i = blockIdx.x * kPlanThreads + tid; i < n_need; i += stride) {
+    const int e = (int)i, b = last_at_or_below(s_need, a.batch, e);
+    const int lp = pages_of(s_have[b], a.page_shift) + (e - s_need[b]);
     a.block_table[(int64_t)b * a.max_pages + lp] = taken(e);
   }
   for (int64_t i0 = (int64_t)blockIdx.x * kPlanTokens + 4 * tid; i0 < a.capacity;
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
         pos[j] = s_have[b] + ((int)i - s_start[b]);
         const int lp = pos[j] >> a.page_shift;
         if (b != seen_b || lp != seen_lp) {
-          const int first = (s_have[b] + page_mask) >> a.page_shift;
+          const int first = pages_of(s_have[b], a.page_shift);
           if (lp >= first) {
             pg = taken(s_need[b] + lp - first);
           } else {

@@ -187,6 +187,39 @@ def test_plan_of_many_tokens_captured_in_place():
     assert table.block_table.tolist() == ref_table
 
 
+@pytest.mark.parametrize("new", [3, 4])
+def test_plan_behind_the_last_tokens_an_int_counts(new):
+    """A page in use whose end is position 2^31 - 1 (the table names one page
+    again and again: a request may be longer than the pool)."""
+    have, page = 2 ** 31 - 5, 16
+    bt = torch.zeros(1, 2 ** 27, dtype=torch.int32, device=DEV)
+    bt[0, -1] = 7
+    table = W.PageTable(bt, i32([have]), i32([3, 2, 1]), i32([3]), page, 20)
+    ws = W.serve_workspace(DEV)
+    plan = W.plan_pages(table, i32([new]), 6, ws=ws)
+    assert W.read_device_status(ws) == 0
+    assert plan.slot_map.tolist() == [7 * 16 + 11 + i for i in range(new)] + [-1] * (6 - new)
+    assert plan.positions.tolist() == [have + i for i in range(new)] + [-1] * (6 - new)
+    assert plan.seq_lens.tolist() == [have + new] and int(plan.n_free) == 3
+    # one more token does not fit an int
+    W.plan_pages(table, i32([5]), 6, ws=ws)
+    assert W.read_device_status(ws) == W.WI_DEV_BAD_SLOT
+
+
+def test_plan_of_as_many_pages_as_an_int_counts():
+    n = 2 ** 31 - 1
+    table = W.PageTable.empty(1, n, 1, n, DEV)
+    ws = W.serve_workspace(DEV)
+    plan = W.plan_pages(table, i32([n]), n, ws=ws)
+    assert W.read_device_status(ws) == 0
+    assert plan.starts.tolist() == [0, n] and plan.seq_lens.tolist() == [n] and int(plan.n_free) == 0
+    step = 1 << 28
+    for i in range(0, n, step):
+        want = torch.arange(i, min(n, i + step), dtype=torch.int32, device=DEV)
+        for got in (plan.slot_map, plan.positions, table.block_table[0]):
+            assert torch.equal(got[i:i + step], want)
+
+
 # ---------------------------------------------------------------- appends
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
