@@ -474,7 +474,8 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * The queries of sequence b are those of its last q_lens[b] tokens: query i
  * sits at position T_b - q_lens[b] + i and attends every position up to its
  * own.  q_lens[b] = T_b is a whole prompt, 1 a decode step, 0 leaves the
- * sequence out (an empty one, T_b = 0, is left out too).  For query head g, KV head g / G:
+ * sequence out (an empty one, T_b = 0, is left out too); T_b <= 2^31 - 256.
+ * For query head g, KV head g / G:
  *   out = sum_p softmax_p(q . k_p / sqrt(d)) v_p,  lse = ln sum_p e^(q . k_p / sqrt(d))
  * q:   device [sum q_lens][Hq][d] in the KV dtype, sequences in order, token
  *      rows q_stride elements apart.

@@ -333,7 +333,9 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
   for (int b = 0; b < kv->batch; ++b) {
     const int T = kv->seq_lens[b], n = p->q_lens ? p->q_lens[b] : T;
     if (n < 0 || n > T) return WI_ERR_INVALID_ARG;
-    if (n > INT32_MAX / G) return WI_ERR_UNSUPPORTED;   // rows are counted in 32 bits
+    // rows are counted in 32 bits, and so are the positions of whole key tiles
+    // (with one behind the last)
+    if (n > INT32_MAX / G || T > INT32_MAX - 255) return WI_ERR_UNSUPPORTED;
     if (n > 0) {
       AttendSeq& s = pl.seq[pl.n_seq++];
       s.b = b; s.T = T; s.n = n; s.q0 = q0;

@@ -129,6 +129,15 @@ def test_attend_refusals(kv, p, expect):
     assert attend_size(kv_struct(**kv), attend_params(**p))[0] == expect
 
 
+@pytest.mark.parametrize("T,expect", [
+    (2 ** 31 - 256, W.WI_OK), (2 ** 31 - 255, W.WI_ERR_UNSUPPORTED), (2 ** 31 - 1, W.WI_ERR_UNSUPPORTED),
+])
+@pytest.mark.parametrize("n", [1, 2000])
+def test_attend_positions_fit_whole_tiles(T, n, expect):
+    kv = kv_struct(seq=[T], n_kv_heads=1, page_size=1024, max_pages=2 ** 21)
+    assert attend_size(kv, attend_params(8, q_lens=[n]))[0] == expect
+
+
 def test_attend_rejects_before_any_cuda_call():
     lib, kv, p = W.lib(), kv_struct(), attend_params(q_lens=[1])
     st, need = attend_size(kv, p)
