@@ -621,6 +621,22 @@ def _token_rows(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
     return row
 
 
+_DEV_BITS = {WI_DEV_BAD_PAGE: "WI_DEV_BAD_PAGE", WI_DEV_BAD_SLOT: "WI_DEV_BAD_SLOT",
+             WI_DEV_TIMEOUT: "WI_DEV_TIMEOUT", WI_DEV_NO_PAGES: "WI_DEV_NO_PAGES"}
+
+
+def _raise_status(ws: torch.Tensor, where: str):
+    """For a serving call that made its workspace itself: nobody else can read
+    the status in it, so the call waits and raises.  (Not while a stream is
+    captured: nothing has run yet.)"""
+    if torch.cuda.is_current_stream_capturing():
+        return
+    flags = read_device_status(ws)
+    if flags:
+        bits = ", ".join(name for bit, name in _DEV_BITS.items() if flags & bit)
+        raise WaveIndexError(WI_ERR_DEVICE_CHECK, f"{where} ({bits})")
+
+
 # The current stream's handle, without making a Stream object of it (3 us a
 # call) where torch has the accessor its own generated code uses.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -691,7 +707,10 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
     and table.n_free advance too with update (or with an `out` that holds them),
     else the plan returns the new ones.  `capacity` bounds the step's tokens;
     slots and positions behind the last one are -1.  A step that does not fit
-    plans nothing and sets WI_DEV_NO_PAGES in the workspace's status."""
+    plans nothing and sets WI_DEV_NO_PAGES in the workspace's status: with a
+    `ws` of the caller's, read_device_status(ws) tells; without one the call
+    waits for the GPU and raises WaveIndexError (a captured call cannot: give it
+    a `ws`)."""
     bt = table.block_table
     dev = _device_of("block_table", bt)
     s = _elsewhere(dev, stream)
@@ -707,7 +726,8 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
         raise ValueError("update: `out` must hold the table's own seq_lens and n_free")
     slots, positions, starts, sl_out, n_free_out = (out.slot_map, out.positions, out.starts,
                                                     out.seq_lens, out.n_free)
-    if ws is None:
+    mine = ws is None
+    if mine:
         ws = serve_workspace(bt.device)
     # one expression on the way of a call that is right (2 us less a call);
     # the checks that name the argument otherwise
@@ -738,6 +758,8 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
                    slots.data_ptr(), positions.data_ptr())
     _check(_lib.wi_plan_pages(C.byref(p), ws.data_ptr(), ws.numel(),
                               _current_stream(dev)), "wi_plan_pages")
+    if mine:
+        _raise_status(ws, "wi_plan_pages")
     return out
 
 
@@ -745,7 +767,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
               v_pool: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """Write k, v [tokens][n_kv_heads][head_dim] into the pools' rows at
     slot_map [tokens] (wi_append_kv).  Negative slots are skipped; k and v may
-    be views of a fused projection's rows."""
+    be views of a fused projection's rows.  A slot outside the pool is skipped
+    and told as plan_pages tells a step that does not fit."""
     dev = k_pool.get_device()
     s = _elsewhere(dev, stream)
     if s is not None:
@@ -764,13 +787,16 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pool: 
     if not (k.shape == v.shape == (n, H, d)):
         raise ValueError(f"k, v: [tokens][{H}][{d}] is expected")
     _on_gpu("slot_map", slot_map, torch.int32, dev, (n,))
-    if ws is None:
+    mine = ws is None
+    if mine:
         ws = serve_workspace(k_pool.device)
     _on_gpu("ws", ws, torch.uint8, dev)
     a = WiKVAppend(_dtype_code(k_pool.dtype), n, H, d, P, n_pages, k.data_ptr(), v.data_ptr(),
                    ks, vs, slot_map.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr())
     _check(_lib.wi_append_kv(C.byref(a), ws.data_ptr(), ws.numel(),
                              _current_stream(dev)), "wi_append_kv")
+    if mine:
+        _raise_status(ws, "wi_append_kv")
 
 
 @dataclass
@@ -819,7 +845,8 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     cache (wi_attend): q [sum q_lens][n_q_heads][head_dim] in the KV dtype,
     sequences in order (rows may be views of wider ones) -> out like q, lse
     fp32 [sum q_lens][n_q_heads].  q may have rows behind the last sequence
-    (a padded batch): out and lse keep theirs."""
+    (a padded batch): out and lse keep theirs.  A page outside the pool reads
+    as zeros and is told as plan_pages tells a step that does not fit."""
     kp = kv.k_pool
     dev = kp.get_device()
     s = _elsewhere(dev, stream)
@@ -848,13 +875,16 @@ def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[tor
     if lse is None:
         lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
     _on_gpu("lse", lse, torch.float32, dev, (n, Hq))
-    if ws is None:
+    mine = ws is None
+    if mine:
         ws = attend_workspace(kv, params)
     _on_gpu("ws", ws, torch.uint8, dev)
     c, p = kv._struct(), params.c_struct(qs, os_)
     _check(_lib.wi_attend(q.data_ptr(), C.byref(c), C.byref(p), out.data_ptr(), lse.data_ptr(),
                           ws.data_ptr(), ws.numel(), _current_stream(dev)),
            "wi_attend")
+    if mine:
+        _raise_status(ws, "wi_attend")
     return out, lse
 
 

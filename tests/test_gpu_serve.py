@@ -255,6 +255,38 @@ def test_append_slot_outside_the_pool_is_skipped():
     W.append_kv(k[:0], k[:0], i32([]), pools[0], pools[1], ws=ws)
 
 
+def test_without_a_workspace_a_call_tells_what_is_wrong():
+    table = make_table([20, 5], 16, 8, 8, 67)
+    table.n_free.fill_(0)
+    before = table.block_table.clone()
+    with pytest.raises(W.WaveIndexError, match="wi_plan_pages .WI_DEV_NO_PAGES") as e:
+        W.plan_pages(table, i32([30, 1]), 40, update=True)
+    assert e.value.status == W.WI_ERR_DEVICE_CHECK and torch.equal(table.block_table, before)
+    pools, k = torch.zeros(2, 4, 2, 16, 64, device=DEV), torch.ones(3, 2, 64, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        with pytest.raises(W.WaveIndexError, match="WI_DEV_BAD_SLOT"):
+            W.append_kv(k, k, i32([64, 5, -1]), pools[0], pools[1], stream=stream)
+        kv = W.KVCache(pools[0], pools[1], i32([[0, 4]]), [20])
+        q = torch.zeros(1, 2, 64, device=DEV)
+        torch.cuda.synchronize()
+        with pytest.raises(W.WaveIndexError, match="wi_attend .WI_DEV_BAD_PAGE"):
+            W.attend(q, kv, W.AttendParams(2, [1]), stream=stream)
+    kv.block_table[0, 1] = 3
+    W.attend(q, kv, W.AttendParams(2, [1]))
+    # captured, nothing has run that could be told
+    g = torch.cuda.CUDAGraph()
+    slots = i32([7, 8, 9])
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        W.append_kv(k, k, slots, pools[0], pools[1])
+        W.attend(q, kv, W.AttendParams(2, [1]))
+    g.replay()
+    torch.cuda.synchronize()
+    assert (pools[:, 0, :, 7:10] == 1).all()
+
+
 # -------------------------------------------------------------- attention
 
 def make_cache(lens, H, d, page, dtype, seed, stale=float("nan"), spread=1.0):
