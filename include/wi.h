@@ -492,8 +492,13 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * finite output as long as the sum of a channel's |v| is below 2^127.  A block-table entry outside the pool reads as zero
  * rows and sets WI_DEV_BAD_PAGE.  Sequences with few query rows have their
  * keys split over the SMs and joined in a fixed order: results do not change
- * from run to run.  Workspace: wi_attend_workspace_size for the same cache
- * and parameters.
+ * from run to run.
+ * Workspace: wi_attend_workspace_size for the same cache and parameters.  It is
+ * not monotone: a sequence's keys may be split into more runs, or at all, when
+ * it or another is shorter or has fewer queries.  wi_attend_workspace_bound is
+ * enough for every call of up to `batch` sequences of up to max_seq_len tokens
+ * with up to max_q_len query tokens each (and grows with each of the three): the
+ * size of one buffer for all steps.
  */
 typedef struct wi_attend_params {
   int32_t n_q_heads;           /* Hq, a multiple of Hkv with G in {1,2,4,8}     */
@@ -505,6 +510,9 @@ typedef struct wi_attend_params {
 } wi_attend_params;
 
 wi_status wi_attend_workspace_size(const wi_kv_cache *kv, const wi_attend_params *p, size_t *bytes);
+wi_status wi_attend_workspace_bound(wi_dtype dtype, int32_t batch, int32_t n_kv_heads,
+                                    int32_t head_dim, int32_t n_q_heads, int32_t max_seq_len,
+                                    int32_t max_q_len, size_t *bytes);
 wi_status wi_attend(const void *q, const wi_kv_cache *kv, const wi_attend_params *p, void *out,
                     float *lse, void *ws, size_t ws_bytes, wi_stream_t stream);
 

@@ -52,7 +52,8 @@ EXPORTED = [
     "wi_decode_workspace_size", "wi_decode_workspace_layout", "wi_decode", "wi_decode_host",
     "wi_decode_stage_count", "wi_decode_stage_name", "wi_read_device_status",
     "wi_status_string", "wi_last_error_string", "wi_decode_noalloc",
-    "wi_plan_pages", "wi_append_kv", "wi_attend_workspace_size", "wi_attend",
+    "wi_plan_pages", "wi_append_kv", "wi_attend_workspace_size", "wi_attend_workspace_bound",
+    "wi_attend",
 ]
 
 
@@ -145,6 +146,8 @@ _sig = {
     "wi_append_kv": (C.c_int, [C.POINTER(WiKVAppend), _P, C.c_size_t, _P]),
     "wi_attend_workspace_size": (C.c_int, [C.POINTER(WiKVCache), C.POINTER(WiAttendParams),
                                            C.POINTER(C.c_size_t)]),
+    "wi_attend_workspace_bound": (C.c_int, [C.c_int, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                            C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     "wi_attend": (C.c_int, [_P, C.POINTER(WiKVCache), C.POINTER(WiAttendParams), _P, _P, _P,
                             C.c_size_t, _P]),
     "wi_decode_stage_count": (C.c_int32, []),
@@ -836,7 +839,20 @@ def attend_workspace_bytes(kv: KVCache, params: AttendParams) -> int:
 
 
 def attend_workspace(kv: KVCache, params: AttendParams) -> torch.Tensor:
+    """Workspace of attend for this cache's lengths and these parameters (other
+    lengths, shorter ones too, may need more: attend_workspace_bound)."""
     return workspace(attend_workspace_bytes(kv, params), kv.k_pool.device)
+
+
+def attend_workspace_bound(kv: KVCache, n_q_heads: int, max_seq_len: int, max_q_len: int) -> int:
+    """Bytes that are enough for every attend over such a cache (its type, heads
+    and number of sequences) with up to max_seq_len tokens and max_q_len query
+    tokens a sequence: one `workspace` of them serves all steps."""
+    n = C.c_size_t()
+    _check(_lib.wi_attend_workspace_bound(_dtype_code(kv.k_pool.dtype), len(kv.seq_lens),
+                                          kv.n_kv_heads, kv.head_dim, n_q_heads, max_seq_len,
+                                          max_q_len, C.byref(n)), "wi_attend_workspace_bound")
+    return n.value
 
 
 def attend(q: torch.Tensor, kv: KVCache, params: AttendParams, out: Optional[torch.Tensor] = None,

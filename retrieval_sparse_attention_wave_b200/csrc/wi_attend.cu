@@ -425,14 +425,18 @@ cudaError_t launch_merge(const AttendTable<N>& tb, int n_rows, const AttendOut& 
 // 3.5 times that, a part of 256 rows (133 KB) and its merge 3 times.
 // fp32: 64 rows, or 16 where no block has more to fill.  An item's fixed part
 // (about 5 us) is two tiles of 64 rows, or six of 16.
+// Split items: over 60000 drawn calls of up to 256 sequences and 300000 tokens
+// the rule alone chose up to 3200 of 16 rows, 2020 of 128 or 256, 14848 and
+// 12548 (fp32); the bounds are a little above those (bf16, d = 128: a workspace
+// of at most 34 and 315 MB).
 AttendShape attend_shape(int dtype, int D, int most) {
   if (dtype == WI_BF16) {
-    if (most <= 16) return AttendShape{16, 128, 148, 2.0, 0.2};
+    if (most <= 16) return AttendShape{16, 128, 148, 2.0, 0.2, 4096};
     const int rows = most <= 128 ? 128 : 256;
-    return AttendShape{rows, 128, 148, 3.5, 3.0 * rows / 256};
+    return AttendShape{rows, 128, 148, 3.5, 3.0 * rows / 256, 2368};
   }
-  if (most <= 16) return AttendShape{16, D == 128 ? 32 : 64, 4 * 148, 6.0, 1.0};
-  return AttendShape{64, D == 128 ? 32 : 64, (D == 128 ? 2 : 3) * 148, 2.0, 0.5};
+  if (most <= 16) return AttendShape{16, D == 128 ? 32 : 64, 4 * 148, 6.0, 1.0, 16384};
+  return AttendShape{64, D == 128 ? 32 : 64, (D == 128 ? 2 : 3) * 148, 2.0, 0.5, 13312};
 }
 
 namespace {

@@ -2,6 +2,7 @@
 // wi_append_kv and wi_attend, and the page-plan and append kernels.
 // Every argument error is detected here, on the host, before any CUDA call.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -283,13 +284,17 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   if ((double)longest + sh.item_cost <= total / slots) return;   // enough blocks
   auto cost = [&](int64_t C) {
     double items = 0, parts = 0;   // parts in full blocks
+    int64_t split = 0;             // items of split sequences
     for (int i = 0; i < pl.n_seq; ++i) {
       const AttendSeq& s = pl.seq[i];
       const uint32_t c = (uint32_t)C;
       const double runs = 0.5 * (double)((most[i] + c - 1) / c + (least[i] + c - 1) / c);
       items += s.nblk * pl.hkv * runs;
+      const int64_t ns = (most[i] + c - 1) / c;
+      if (ns > 1) split += ns * s.nblk * pl.hkv;
       if (runs > 1) parts += pl.hkv * runs * std::min<double>((double)s.n * pl.G / R, s.nblk);
     }
+    if (split > sh.most_split) return HUGE_VAL;
     const double one = (double)std::min(C, longest) + sh.item_cost, spread = sh.part_cost * parts / slots;
     const double t = items <= slots ? one : (total + items * sh.item_cost) / slots + 0.5 * one;
     return t + spread + (C < longest ? kMergeCost : 0);
@@ -297,7 +302,7 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
   int64_t best = longest;
   double cheapest = cost(longest);
   // (a candidate costs two divisions a sequence: all 147 for up to two
-  // sequences, 29 or 17 of them for more)
+  // sequences, 27 or 17 of them for more)
   const int coarse = pl.n_seq <= 2 ? kMaxSplit + 1 : pl.n_seq <= 32 ? 8 : 4;
   for (int k = 2; k <= kMaxSplit; k += 1 + k / coarse) {
     const int64_t C = cdiv(longest, k);
@@ -310,6 +315,25 @@ void choose_splits(AttendPlan& pl, const AttendShape& sh) {
     s.ns = (int)cdiv(most[i], best);
     s.run = (int)cdiv(most[i], s.ns);
   }
+}
+
+// The most part rows of a call of up to `batch` sequences with at most n query
+// tokens and T tokens each, in blocks of sh.rows rows: those of make_attend_plan
+// with every sequence split as far as choose_splits ever does.
+int64_t most_parts(const AttendShape& sh, int batch, int hkv, int G, int64_t T, int64_t n) {
+  const int64_t rows = n * G, nblk = cdiv(rows, sh.rows);
+  const int64_t ns = std::min<int64_t>(kMaxSplit, cdiv(cdiv(T, sh.keys), kMinTiles));
+  if (ns < 2) return 0;
+  const int64_t full = std::min<int64_t>(sh.rows, rows);
+  return full * (int64_t)std::min((double)sh.most_split, (double)batch * hkv * nblk * ns);
+}
+
+size_t attend_bytes(int64_t parts, int D, size_t* off_ml, size_t* off_o) {
+  size_t o = 256;
+  auto take = [&](size_t bytes) { const size_t r = o; o = align_up(o + bytes, 256); return r; };
+  *off_ml = take((size_t)parts * 8);
+  *off_o = take((size_t)parts * D * 4);
+  return o;
 }
 
 wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, AttendPlan& pl) {
@@ -367,11 +391,7 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
   pl.n_items = (int)items;
   pl.n_merge_rows = (int)mrows;
   pl.q_tokens = q0;
-  size_t o = 256;
-  auto take = [&](size_t bytes) { const size_t r = o; o = align_up(o + bytes, 256); return r; };
-  pl.off_ml = take((size_t)parts * 8);
-  pl.off_o = take((size_t)parts * pl.D * 4);
-  pl.total = o;
+  pl.total = attend_bytes(parts, pl.D, &pl.off_ml, &pl.off_o);
   return WI_OK;
 }
 
@@ -463,6 +483,29 @@ wi_status wi_attend_workspace_size(const wi_kv_cache* kv, const wi_attend_params
   const wi_status st = make_attend_plan(kv, p, pl);
   if (st != WI_OK) return st;
   *bytes = pl.total;
+  return WI_OK;
+}
+
+wi_status wi_attend_workspace_bound(wi_dtype dtype, int32_t batch, int32_t n_kv_heads, int32_t head_dim,
+                                    int32_t n_q_heads, int32_t max_seq_len, int32_t max_q_len, size_t* bytes) {
+  if (!bytes || (dtype != WI_F32 && dtype != WI_BF16) || batch < 1 || n_kv_heads < 1 || head_dim < 1 ||
+      n_q_heads < 1 || n_q_heads % n_kv_heads != 0 || max_seq_len < 0 || max_q_len < 0)
+    return WI_ERR_INVALID_ARG;
+  const int G = n_q_heads / n_kv_heads;
+  if (batch > kMaxBatch || (head_dim != 64 && head_dim != 128) || (G != 1 && G != 2 && G != 4 && G != 8))
+    return WI_ERR_UNSUPPORTED;
+  const int64_t n = std::min(max_q_len, max_seq_len);
+  // a call may have fewer rows than these, so every shape of fewer counts
+  int64_t parts = 0, below = -1;
+  for (int64_t most : {(int64_t)16, (int64_t)128, n * G}) {
+    most = std::min(most, n * G);
+    if (most <= below) continue;
+    below = most;
+    const AttendShape sh = attend_shape(dtype, head_dim, (int)std::min<int64_t>(most, INT32_MAX));
+    parts = std::max(parts, most_parts(sh, batch, n_kv_heads, G, max_seq_len, most / G));
+  }
+  size_t ml, o;
+  *bytes = attend_bytes(parts, head_dim, &ml, &o);
   return WI_OK;
 }
 

@@ -77,10 +77,12 @@ struct AttendArgs {
 // Rows per block, keys per tile and items running at once, for a call whose
 // blocks have at most `most` rows to fill (wi_attend.cu); in times of a key
 // tile of a full block, what an item costs besides its tiles and what writing
-// and merging a full block's part costs.
+// and merging a full block's part costs; and the most items that the split
+// sequences of a call have together, which bounds the workspace.
 struct AttendShape {
   int rows, keys, slots;
   double item_cost, part_cost;
+  int most_split;
 };
 AttendShape attend_shape(int dtype, int D, int most);
 cudaError_t launch_attend(const AttendPlan& pl, const AttendArgs& a, cudaStream_t s);

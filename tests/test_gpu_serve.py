@@ -688,6 +688,18 @@ def test_attend_range_of_values(dtype, q_len, rise, exact):
         S.assert_attend(out.double() * 2.0 ** -power, lse, ref, dtype, T, d)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_workspace_of_the_bound_serves_all_steps(dtype):
+    """Growing contexts, chunks and single tokens, sequences that come and go."""
+    H, G, d, page, top, most = 2, 4, 128, 16, 6000, 70
+    kv = make_cache([top, top, 900], H, d, page, dtype, 41)
+    ws = W.workspace(W.attend_workspace_bound(kv, H * G, top, most), DEV)
+    for lens, q_lens in (([70, 70, 0], [70, 70, 0]), ([513, 600, 0], [70, 1, 0]), ([4366, 30, 900], [1, 30, 1]),
+                         ([4657, 31, 0], [1, 1, 0]), ([6000, 6000, 900], [1, 1, 1]), ([6000, 5000, 2], [70, 3, 2])):
+        step = W.KVCache(kv.k_pool, kv.v_pool, kv.block_table, lens)
+        check_attend(step, make_q(sum(q_lens), H * G, d, dtype, sum(lens)), q_lens, ws=ws)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

@@ -166,6 +166,67 @@ def test_attend_splits_only_where_blocks_are_few():
     assert st == W.WI_OK and n == 256
 
 
+def attend_bound(batch, max_seq, max_q, dtype=W.WI_BF16, H=8, d=128, Hq=32):
+    n = C.c_size_t()
+    return W.lib().wi_attend_workspace_bound(dtype, batch, H, d, Hq, max_seq, max_q, C.byref(n)), n.value
+
+
+def test_attend_workspace_is_not_monotone_in_the_lengths():
+    """What wi_attend_workspace_bound is for: one token over 4366 keys needs more
+    than over 4657, a chunk of 512 nothing at the start of its prompt."""
+    size = lambda T, n: attend_size(kv_struct(seq=[T]), attend_params(q_lens=[n]))[1]  # noqa: E731
+    assert size(4366, 1) > size(4657, 1) and size(512, 512) < size(2048, 512)
+
+
+@pytest.mark.parametrize("dtype", [W.WI_BF16, W.WI_F32])
+@pytest.mark.parametrize("H,G,d", [(8, 4, 128), (1, 1, 64), (16, 8, 128)])
+@pytest.mark.parametrize("batch", [1, 16, 200])
+def test_attend_workspace_bound_holds(dtype, H, G, d, batch):
+    """For whole batches and parts of them, decode steps, chunks, prompts and
+    mixtures, at every length up to the bound's."""
+    import random
+    rng = random.Random(f"{dtype} {H} {d} {batch}")
+    over = dict(dtype=dtype, n_kv_heads=H, head_dim=d, page_size=1024, max_pages=1 << 20)
+    seen = 256
+    for _ in range(40):
+        top = int(2 ** rng.uniform(0, 17))
+        most = min(top, int(2 ** rng.uniform(0, 12)))
+        st, bound = attend_bound(batch, top, most, dtype, H, d, H * G)
+        assert st == W.WI_OK and bound % 256 == 0
+        for _ in range(8):
+            lens = [rng.randint(0, top) if rng.random() < 0.5 else top for _ in range(rng.randint(1, batch))]
+            step = rng.choice([1, most])
+            q_lens = [min(T, rng.choice([0, 1, step, most])) for T in lens]
+            st, n = attend_size(kv_struct(seq=lens, **over), attend_params(H * G, q_lens=q_lens))
+            assert st == W.WI_OK and n <= bound
+            seen = max(seen, n)
+    assert seen > 256
+
+
+def test_attend_workspace_bound_grows_and_is_moderate():
+    for dtype in (W.WI_BF16, W.WI_F32):
+        for k, far in ((0, 256), (1, 1 << 20), (2, 4096)):
+            at, last = [16, 20000, 40], 0
+            for x in sorted({1, 2, 3, 5, 16, 17, 31, 32, 33, 64, 65, 100, 256, far}):
+                at[k] = min(x, far)
+                n = attend_bound(*at, dtype=dtype)[1]
+                assert n >= last
+                last = n
+    assert attend_bound(1, 131072, 1)[1] < 3e6 and attend_bound(256, 1 << 20, 4096)[1] < 3.2e8
+    assert attend_bound(64, 256, 256)[1] == 256      # two tiles of keys are never split
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(), W.WI_OK), (dict(batch=0), W.WI_ERR_INVALID_ARG), (dict(batch=257), W.WI_ERR_UNSUPPORTED),
+    (dict(dtype=7), W.WI_ERR_INVALID_ARG), (dict(H=0), W.WI_ERR_INVALID_ARG), (dict(d=96), W.WI_ERR_UNSUPPORTED),
+    (dict(Hq=12), W.WI_ERR_INVALID_ARG), (dict(Hq=24), W.WI_ERR_UNSUPPORTED),
+    (dict(max_seq=-1), W.WI_ERR_INVALID_ARG), (dict(max_q=-1), W.WI_ERR_INVALID_ARG),
+    (dict(max_seq=0, max_q=0), W.WI_OK), (dict(max_seq=2 ** 31 - 1, max_q=2 ** 31 - 1), W.WI_OK),
+])
+def test_attend_workspace_bound_refusals(over, expect):
+    assert attend_bound(**{**dict(batch=4, max_seq=100, max_q=10), **over})[0] == expect
+
+
 def test_python_checks_name_the_argument():
     kv = W.KVCache(torch.zeros(4, 2, 16, 64), torch.zeros(4, 2, 16, 64),
                    torch.zeros(1, 4, dtype=torch.int32), [40])
