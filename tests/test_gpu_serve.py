@@ -700,6 +700,28 @@ def test_one_workspace_of_the_bound_serves_all_steps(dtype):
         check_attend(step, make_q(sum(q_lens), H * G, d, dtype, sum(lens)), q_lens, ws=ws)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("batch,T,n,H,G", [(24, 4096, 1, 1, 8), (40, 3000, 2, 2, 1), (24, 2300, 17, 1, 8)])
+def test_attend_splits_keys_of_more_than_16_sequences(dtype, batch, T, n, H, G):
+    """Both joins (2720 rows, of 20 sequences with queries, are many) behind the kernels of
+    large batches."""
+    lens = [T - 37 * (b % 5) for b in range(batch)]
+    q_lens = [n if b % 7 else 0 for b in range(batch)]
+    kv = make_cache(lens, H, 128, 16, dtype, batch)
+    assert W.attend_workspace_bytes(kv, W.AttendParams(H * G, q_lens)) > 256
+    check_attend(kv, make_q(sum(q_lens), H * G, 128, dtype, batch), q_lens)
+
+
+@pytest.mark.parametrize("dtype,T,d,n", [(BF16, 131072, 128, 1), (BF16, 131000, 64, 1), (BF16, 131072, 128, 17),
+                                         (F32, 40000, 128, 1), (F32, 79999, 64, 1)])
+def test_attend_of_more_than_128_runs(dtype, T, d, n):
+    """A join of more parts than one round of its four warps takes."""
+    kv = make_cache([T], 1, d, 16, dtype, 43)
+    size = W.attend_workspace_bytes(kv, W.AttendParams(1, [n]))
+    assert size > 256 + 128 * n * (8 + 4 * d)
+    check_attend(kv, make_q(n, 1, d, dtype, 43), [n])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
