@@ -48,22 +48,38 @@ def measured_peaks():
     return {"hbm_gbs": FALLBACK_HBM_GBS, "bf16_tflops": FALLBACK_BF16_TFLOPS}, "fallback"
 
 
-def kernel_source_sha256() -> str:
-    """Hash of the CUDA sources (csrc/*.cu, *.cuh, *.h) in file-name order,
-    comments and blank lines left out: a comment edit does not change the
-    compiled kernels, so it keeps the measured traffic valid."""
+def decode_sources():
+    """The sources of the decode's kernels and plans: wi_decode*, wi_api.cu and
+    what they include in csrc (but the serving calls' declarations)."""
     import glob
+    import re
+    csrc = os.path.join(ROOT, "retrieval_sparse_attention_wave_b200", "csrc")
+    todo = glob.glob(os.path.join(csrc, "wi_decode*")) + [os.path.join(csrc, "wi_api.cu")]
+    found = set()
+    while todo:
+        f = todo.pop()
+        if f in found or not os.path.exists(f) or os.path.basename(f) == "wi_serve.h":
+            continue
+        found.add(f)
+        with open(f) as fh:
+            todo += [os.path.join(csrc, x) for x in re.findall(r'#include "([^"]+)"', fh.read())]
+    return sorted(found)
+
+
+def kernel_source_sha256() -> str:
+    """Hash of the decode's sources in file-name order, comments and blank lines
+    left out: a comment edit, or another operator's, does not change the decode's
+    compiled kernels, so it keeps their measured traffic valid."""
     import hashlib
     import re
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "retrieval_sparse_attention_wave_b200", "csrc", "*"))):
-        if f.endswith((".cu", ".cuh", ".h")):
-            with open(f) as fh:
-                src = fh.read()
-            src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
-            src = re.sub(r"//[^\n]*", "", src)
-            src = "\n".join(line.rstrip() for line in src.splitlines() if line.strip())
-            h.update(src.encode())
+    for f in decode_sources():
+        with open(f) as fh:
+            src = fh.read()
+        src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+        src = re.sub(r"//[^\n]*", "", src)
+        src = "\n".join(line.rstrip() for line in src.splitlines() if line.strip())
+        h.update(src.encode())
     return h.hexdigest()
 
 
