@@ -714,6 +714,8 @@ def plan_pages(table: PageTable, new_lens: torch.Tensor, capacity: int,
     `ws` of the caller's, read_device_status(ws) tells; without one the call
     waits for the GPU and raises WaveIndexError (a captured call cannot: give it
     a `ws`)."""
+    if not 0 <= capacity < 1 << 31:
+        raise ValueError(f"capacity: {capacity} is outside 0..2^31 - 1")
     bt = table.block_table
     dev = _device_of("block_table", bt)
     s = _elsewhere(dev, stream)

@@ -251,6 +251,14 @@ def test_python_checks_name_the_argument():
         W.plan_pages(table, torch.ones(2, dtype=torch.int32), 8)
 
 
+@pytest.mark.parametrize("capacity", [-1, 2 ** 31, 2 ** 32 + 5])
+def test_plan_capacity_fits_an_int(capacity):
+    """(2^32 + 5 went to the library as 5.)"""
+    table = W.PageTable.empty(2, 4, 16, 8, "cpu")
+    with pytest.raises(ValueError, match="capacity"):
+        W.plan_pages(table, torch.ones(2, dtype=torch.int32), capacity)
+
+
 def test_cache_lengths_may_change_between_calls():
     kv = W.KVCache(torch.zeros(4, 2, 16, 64), torch.zeros(4, 2, 16, 64),
                    torch.zeros(2, 4, dtype=torch.int32), [40, 3])
