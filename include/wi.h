@@ -480,7 +480,8 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * q:   device [sum q_lens][Hq][d] in the KV dtype, sequences in order, token
  *      rows q_stride elements apart.
  * out: device, like q with out_stride (KV dtype: the next product's input).
- *      Not q itself.  Rows behind the last sequence are not written.
+ *      No row of it may overlap one of q (beside them in wider rows is fine).
+ *      Rows behind the last sequence are not written.
  * lse: device float [sum q_lens][Hq], or NULL.
  * Keys behind a query's position have no effect on it, whatever they hold
  * (NaN and infinities too), nor have pool rows behind T_b.  bf16: a sequence of

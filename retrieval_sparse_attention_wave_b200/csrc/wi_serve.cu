@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "wi.h"
 #include "wi_common.cuh"
@@ -395,6 +396,23 @@ wi_status make_attend_plan(const wi_kv_cache* kv, const wi_attend_params* p, Att
   return WI_OK;
 }
 
+// n rows of `row` bytes, sa apart from a on and sb apart from b on, share a byte.
+bool rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t n, int64_t row) {
+  if (a > b) {
+    std::swap(a, b);
+    std::swap(sa, sb);
+  }
+  // row i of b against the last row of a that starts at or before it, and the next
+  auto meets = [&](int64_t i) {
+    const int64_t d = (int64_t)(b - a) + i * sb, j = d / sa, r = d - j * sa;
+    return (j < n && r < row) || (j + 1 < n && sa - r < row);
+  };
+  if (sa == sb) return meets(0);   // (the others lie alike, with fewer rows of a beside them)
+  for (int64_t i = 0; i < n && (int64_t)(b - a) + i * sb < (n - 1) * sa + row; ++i)
+    if (meets(i)) return true;
+  return false;
+}
+
 wi_status check_ws(const void* ws, size_t have, size_t need) {
   return !ws || !aligned(ws, 256) || have < need ? WI_ERR_WORKSPACE : WI_OK;
 }
@@ -518,7 +536,10 @@ wi_status wi_attend(const void* q, const wi_kv_cache* kv, const wi_attend_params
   if (pl.n_seq > 0 && (!q || !out || q == out)) return WI_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, pl.total)) != WI_OK) return st;
   if (pl.n_seq == 0) return WI_OK;
-  const int64_t row = (int64_t)pl.Hq * pl.D;
+  const int64_t row = (int64_t)pl.Hq * pl.D, es = pl.dtype == WI_BF16 ? 2 : 4;
+  if (rows_overlap(reinterpret_cast<uintptr_t>(q), (p->q_stride ? p->q_stride : row) * es,
+                   reinterpret_cast<uintptr_t>(out), (p->out_stride ? p->out_stride : row) * es, pl.q_tokens, row * es))
+    return WI_ERR_INVALID_ARG;
   AttendArgs a{};
   a.q = q; a.out = out; a.lse = lse;
   a.q_stride = p->q_stride ? p->q_stride : row;

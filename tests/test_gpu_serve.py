@@ -722,6 +722,23 @@ def test_attend_of_more_than_128_runs(dtype, T, d, n):
     check_attend(kv, make_q(n, 1, d, dtype, 43), [n])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_output_beside_the_queries_in_one_row(dtype):
+    kv = make_cache([70, 90], 2, 64, 16, dtype, 45)
+    wide = make_q(160, 17, 64, dtype, 45)
+    q = wide[:, 1:9].clone()
+    want, _ = W.attend(q, kv, W.AttendParams(8))
+    for first in (9, 0):
+        rows = wide.clone()
+        at = 1 if first else 8
+        rows[:, at:at + 8] = q
+        out = rows[:, first:first + 8]
+        W.attend(rows[:, at:at + 8], kv, W.AttendParams(8), out=out)
+        assert torch.equal(out, want) and torch.equal(rows[:, at:at + 8], q)
+    with pytest.raises(W.WaveIndexError):
+        W.attend(wide[:, 1:9], kv, W.AttendParams(8), out=wide[:, 2:10])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

@@ -155,6 +155,21 @@ def test_attend_rejects_before_any_cuda_call():
     assert lib.wi_attend(None, C.byref(kv), C.byref(none), None, None, FAKE, need, None) == W.WI_OK
 
 
+@pytest.mark.parametrize("q,out,qs,os,n", [
+    (0, 256, 0, 0, 1), (256, 0, 0, 0, 1), (0, 8176, 0, 0, 3), (8192, 16, 0, 0, 1),
+    (0, 8192, 0, 0, 2),                  # the second row of q
+    (16384 - 16, 0, 8192, 8192, 3),      # the last bytes of a row beside it
+    (0, 8192, 6144, 6144, 2),            # 12288 bytes apart: its end is in q's second row
+    (0, 3 * 8192, 8192, 4096, 9), (5 * 8192, 0, 4096, 8192, 9),     # other strides
+])
+def test_attend_refuses_output_rows_over_query_rows(q, out, qs, os, n):
+    """Rows of 8192 bytes; strides in elements of 2 bytes."""
+    kv, p = kv_struct(), attend_params(q_lens=[n], q_stride=qs, out_stride=os)
+    st, need = attend_size(kv, p)
+    base = FAKE + 0x1000000
+    assert W.lib().wi_attend(base + q, C.byref(kv), C.byref(p), base + out, None, FAKE, need, None) == W.WI_ERR_INVALID_ARG
+
+
 def test_attend_splits_only_where_blocks_are_few():
     # a prompt has blocks enough: status word only, no parts
     assert attend_size(kv_struct(seq=[65536]), attend_params())[1] == 256
