@@ -10,8 +10,8 @@
 // values, so 16 bits of it count, as in the decode over an index.  With up to
 // eight rows (a token of a group of eight heads) the second parts are the
 // operand's rows 8..15, so a tile takes as many products as with weights of
-// one part (363 us against 361 for 16 tokens over 32768 keys each; with
-// products of their own 373: the clocks fall under the power cap).  A tile
+// one part (16 tokens over 32768 keys each: 357 us, as before; with products
+// of their own 373, and even masked off 363: the clocks fall).  A tile
 // costs a warp about 250 instructions, a third of the time its 64 KB take to
 // arrive, and a stage is free as soon as eight warps have read it: the
 // tensor-memory kernel holds its stages through a softmax of 128 rows, which
@@ -19,6 +19,7 @@
 // heads of 128: 363 us a call back to back, 5.9 TB/s; one over 131072: 93 us,
 // 6 of them the merge.
 #include <cmath>
+#include <type_traits>
 
 #include "wi_attend_tiles.cuh"
 
@@ -192,7 +193,7 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
       for (int e = 1; e < 4; e += 2) split_bf16(s[e >> 1][2], s[e >> 1][3], hi[e], lo[e]);
     }
     if (!(ok = full())) break;
-    {
+    auto output = [&](auto second) {   // (a branch a product would leave the second ones in the pipe, masked)
       const unsigned char* tile = ring + (size_t)st * S::kTile;
       const int row = 16 * warp + (lane & 15);
 #pragma unroll
@@ -205,13 +206,14 @@ attend_few_kernel(const __grid_constant__ AttendTable<N> tb, const __nv_bfloat16
           for (int e = 0; e < 4; ++e) b[e] = clean(b[e], base + t2 + 8 * (e & 1), first_pos, it.key_end, bad);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mma_bf16_4(o[2 * cb + e], hi[0], hi[1], hi[2], hi[3], b[2 * e], b[2 * e + 1]);
-        if (!narrow) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mma_bf16_4(o[2 * cb + e], lo[0], lo[1], lo[2], lo[3], b[2 * e], b[2 * e + 1]);
+        for (int e = 0; e < 2; ++e) {
+          mma_bf16_4(o[2 * cb + e], hi[0], hi[1], hi[2], hi[3], b[2 * e], b[2 * e + 1]);
+          if (second) mma_bf16_4(o[2 * cb + e], lo[0], lo[1], lo[2], lo[3], b[2 * e], b[2 * e + 1]);
         }
       }
-    }
+    };
+    if (narrow) output(std::false_type{});
+    else output(std::true_type{});
     release();
   }
   if (narrow) {
