@@ -493,7 +493,10 @@ wi_status wi_append_kv(const wi_kv_append *a, void *ws, size_t ws_bytes, wi_stre
  * finite output as long as the sum of a channel's |v| is below 2^127.  A block-table entry outside the pool reads as zero
  * rows and sets WI_DEV_BAD_PAGE.  Sequences with few query rows have their
  * keys split over the SMs and joined in a fixed order: results do not change
- * from run to run.
+ * from run to run.  Lengths are read on the host during the call, and the block
+ * size (16, 128 or 256 query rows of a KV head) is that of the largest sequence:
+ * a captured call serves the lengths it was captured with, and single tokens are
+ * faster in a call without a chunk.
  * Workspace: wi_attend_workspace_size for the same cache and parameters.  It is
  * not monotone: a sequence's keys may be split into more runs, or at all, when
  * it or another is shorter or has fewer queries.  wi_attend_workspace_bound is

@@ -24,8 +24,8 @@ namespace {
 // Products run on packed fp32 FMAs (two head channels at a time).  Bound by
 // issue: a tile of 64 x 64 (D = 64) is 2048 packed FMAs a thread, 4096 clocks
 // of the FMA pipe, and takes about 8000 with its shared-memory reads, powers
-// and four barriers at 2 to 3 warps a scheduler.  39 TFLOP/s at 8192 tokens,
-// 32 heads on 8 KV heads of 128 (14.0 ms); 4096 tokens, one head of 64: 79 us.
+// and four barriers at 2 to 3 warps a scheduler.  42 TFLOP/s at 8192 tokens,
+// 32 heads on 8 KV heads of 128 (13.1 ms); 4096 tokens, one head of 64: 82 us.
 // A block of at most 16 rows keeps two rows a thread, for more CTAs an SM.
 template <int D, int RT>
 struct FmaShape {
@@ -420,6 +420,9 @@ cudaError_t launch_merge(const AttendTable<N>& tb, int n_rows, const AttendOut& 
 
 }  // namespace
 
+// One shape a call, by its largest sequence: a chunk among single tokens puts
+// them in blocks of its size (16 tokens over 32768 keys and a chunk of 512: 745
+// us; in two calls 375 and 248).
 // bf16: 256 rows a block where some sequence has more than a tile of 128.  A
 // tile takes about 2850 clocks; an item's queries, pipeline fill and output
 // 3.5 times that, a part of 256 rows (133 KB) and its merge 3 times.

@@ -16,8 +16,8 @@
 // arrive, and a stage is free as soon as eight warps have read it: the
 // tensor-memory kernel holds its stages through a softmax of 128 rows, which
 // leaves 96 KB in flight and 4.9 TB/s.  16 tokens over 32768 keys each, 8 KV
-// heads of 128: 363 us a call back to back, 5.9 TB/s; one over 131072: 93 us,
-// 6 of them the merge.
+// heads of 128: 357 to 363 us a call back to back, 5.9 to 6.0 TB/s; one over
+// 131072: 92 us, 6 of them the merge.
 #include <cmath>
 #include <type_traits>
 

@@ -106,7 +106,7 @@ __device__ __forceinline__ void load_units(const Item& it, int hkv, const Pool& 
     // arriving two units behind the one being issued.  Lane l looks up rows l,
     // l + 32, l + 64 and l + 96 of a tile, a tile ahead; the copies of a row
     // get its place by a shuffle.  One warp's issue bounds it: 8192 tokens on
-    // pages of one take 750 us, of 16 (tensor copies) 442.
+    // pages of one take 743 us, of 16 (tensor copies) 449.
     constexpr int CH = D / 8, kLag = 2;
     auto arrive = [&](int u) {
       fence_proxy_async();

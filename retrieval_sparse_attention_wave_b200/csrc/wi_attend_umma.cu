@@ -37,9 +37,9 @@
 // clocks (read 170, maximum 250, weights 1220: the special-function unit
 // alone is 768), its output and next scores 1024, the hand-overs 200; the two
 // groups' chains interleave to 2850 clocks a pair of tiles, of which the
-// tensor cores work 2048.  8192 tokens of 32 heads on 8 KV heads of 128: 440
-// us, 1.25 PFLOP/s (518 us back to back under the power cap); 32768 tokens
-// 7.6 ms, 1.15 PFLOP/s.
+// tensor cores work 2048.  8192 tokens of 32 heads on 8 KV heads of 128: 450
+// us, 1.22 PFLOP/s (520 us back to back under the power cap); 32768 tokens
+// 7.6 to 7.7 ms, 1.15 PFLOP/s.
 #include <cmath>
 
 #include "wi_attend_tiles.cuh"

@@ -30,8 +30,9 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // and 16-byte stores.  The first CTA writes the lengths and the stack's size
 // too; where they are updated in place and other CTAs may still be reading
 // them, a kernel of one CTA behind this one does.  Nothing is kept between
-// calls.  Latency bounds it (lengths, scan, page, store): 7.6 us for a step of
-// 64 requests, cold; 335445 tokens 6.0 us.
+// calls.  Latency bounds it (lengths, scan, page, store): 6.5 to 8.3 us for a
+// step of 64 requests, cold; 335445 tokens 4.9 us, and 2.8 for the lengths in
+// place behind it.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 4 * kPlanThreads;   // per CTA and round
 
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanArgs
 // A copy: every thread moves 16-byte chunks, kAppendBatch loads in flight,
 // from token rows (contiguous over the heads) to the heads' page rows.  HBM
 // bounds it: 131072 tokens of 8 heads of 128 (1.07 GB read and written) in
-// 168 us, 6.4 TB/s; 16 tokens 5.2 us.
+// 178 us a call back to back, 6.0 TB/s (169 us of it the kernel, alone and
+// cold); 16 tokens 5.2 us.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendBatch = 8;
 
