@@ -739,6 +739,41 @@ def test_attend_output_beside_the_queries_in_one_row(dtype):
         W.attend(wide[:, 1:9], kv, W.AttendParams(8), out=wide[:, 2:10])
 
 
+@pytest.mark.parametrize("dtype,n", [(BF16, 1), (BF16, 3), (F32, 1)])
+def test_attend_over_the_longest_sequence(dtype, n):
+    """2^31 - 256 tokens on three pages named again and again: equal scores and
+    values of one, so each query's output is one and its mass a count."""
+    T, page, G = 2 ** 31 - 256, 1024, 8
+    k, v = torch.zeros(3, 1, page, 64, dtype=dtype, device=DEV), torch.ones(3, 1, page, 64, dtype=dtype, device=DEV)
+    bt = (torch.arange(2 ** 21, device=DEV) % 3).to(torch.int32)[None]
+    kv = W.KVCache(k, v, bt, [T])
+    out, lse = W.attend(make_q(n, G, 64, dtype, 47), kv, W.AttendParams(G, [n]))
+    assert (out == 1).all()
+    seen = torch.arange(T - n + 1, T + 1, dtype=torch.float64, device=DEV)[:, None]
+    assert ((lse.double() - seen.log()).abs() <= 2.0 ** -22 * 32).all()
+
+
+def test_attend_calls_at_once_on_two_streams():
+    """Split and whole calls side by side, each with a workspace of its own."""
+    calls = []
+    for seed, lens, q_lens, dtype in ((51, [9000, 300], [1, 1], BF16), (52, [2000, 700], [300, 700], BF16),
+                                      (53, [5000], [40], BF16), (54, [3000, 20], [1, 20], F32)):
+        kv, prm = make_cache(lens, 2, 128, 16, dtype, seed), W.AttendParams(8, q_lens)
+        q = make_q(sum(q_lens), 8, 128, dtype, seed)
+        ws = W.attend_workspace(kv, prm)
+        calls.append((q, kv, prm, ws, W.attend(q, kv, prm, ws=ws)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        q, kv, prm, ws, _ = calls[2 * (i // 2 % 2) + i % 2]     # (a workspace stays on one stream)
+        got.append(W.attend(q, kv, prm, ws=ws, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        want, want_lse = calls[2 * (i // 2 % 2) + i % 2][4]
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
