@@ -434,15 +434,14 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
       const bool part = it.part >= 0;
       const int r4 = r - lane + (lane & ~3);
       uint4 x[4];
-      bool lost = false;   // a sum is not finite (exact_weights)
+      float2 odd = make_float2(0.f, 0.f);   // 0, or NaN where a sum is not finite
 #pragma unroll 1
       for (int col = 0; col < D; col += 16) {
         uint32_t y[16];
         tmem_ld16(to + col, y);
-        if (kExact) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) lost |= !isfinite(__uint_as_float(y[e]));
-        }
+        for (int e = 0; e < 8; ++e)
+          odd = __ffma2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(0.f, 0.f), odd);
         if (part) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
@@ -467,13 +466,14 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
           *reinterpret_cast<uint4*>(o + 16 * (lane & 3)) = t[c];
         }
       }
-      lost = lost && real && l == l;   // (a row whose mass is NaN is NaN)
+      const bool lost = odd.x + odd.y != 0.f && real && l == l;   // (a row whose mass is NaN is NaN)
       if (__any_sync(0xffffffffu, lost || *(volatile uint32_t*)&s_bad != 0)) {
         // Values that are not finite, added to the rows that see them (a
-        // positive weight of them is they themselves).  With weights of two
-        // parts, the second 0 or negative, an infinity that every row sees has
-        // made NaN of its column: all of a lost row's keys are looked at, and
-        // the first such value takes its column's place.
+        // positive weight of them is they themselves).  An infinity that every
+        // row sees has made NaN of its column where its weight, or the second
+        // part of it, came out as 0 or that part is negative: all of a lost
+        // row's keys are looked at, and the first such value takes its
+        // column's place.
         __syncwarp();
         const int p1 = real ? min(pos + 1, it.t1 * kRows) : 0;
         uint32_t found[D / 32] = {};
@@ -489,7 +489,7 @@ attend_umma_kernel(const __grid_constant__ AttendTable<N> tb, const __grid_const
             }
             const float f = __bfloat162float(*v);
             if (isfinite(f)) continue;
-            const bool first = kExact && !((found[c / 32] >> (c % 32)) & 1u);
+            const bool first = lost && !((found[c / 32] >> (c % 32)) & 1u);
             found[c / 32] |= 1u << (c % 32);
             if (part) {
               float* o = ao.o + (it.part + r) * D + c;

@@ -774,6 +774,25 @@ def test_attend_calls_at_once_on_two_streams():
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("n,exact", [(1, False), (20, False), (260, False), (260, True)])
+@pytest.mark.parametrize("gap", [90, 110, 140])
+def test_attend_infinite_value_of_a_small_weight(n, exact, gap):
+    """An infinity under a weight of 2^-gap of the largest is infinite, not 0
+    times it."""
+    T, d, G = 900, 64, 4
+    kv = steps_cache(T, d, BF16, 55, gap)
+    q = torch.zeros(n, G, d, dtype=BF16, device=DEV)
+    q[:, :, 0] = 1
+    prm = W.AttendParams(G, [n], exact_weights=exact)
+    clean, _ = W.attend(q, kv, prm)
+    for at, c in ((5, 3), (300, 8)):            # keys of score 0
+        kv.v_pool[int(kv.block_table[0, at // 16]), 0, at % 16, c] = math.inf
+    out, lse = W.attend(q, kv, prm)
+    assert torch.isfinite(lse).all() and (out[:, :, 3] == math.inf).all() and (out[:, :, 8] == math.inf).all()
+    rest = [c for c in range(d) if c not in (3, 8)]
+    assert torch.equal(out[:, :, rest], clean[:, :, rest])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
